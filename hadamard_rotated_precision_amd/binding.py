@@ -1,5 +1,5 @@
-"""Thin ctypes binding of libhq (include/hq.h): the same entry-point names, argument
-marshalling only. Every step of the computation runs in the HIP kernels behind the C ABI;
+"""Thin ctypes binding of libhq (include/hq.h) and libhq_train (include/hq_train.h): the same
+entry-point names, argument marshalling only. Every step of the computation runs in the HIP kernels behind the C ABI;
 torch is used by the helpers below only to allocate device memory and to name streams.
 
 Loading fails loudly when the library is missing and cannot be built: there is no fallback.
@@ -11,6 +11,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 # HQ_LIB_PATH names another build of the same sources (the host-sanitizer test's); there is
 # still no fallback when the named library is missing
 LIB_PATH = os.environ.get("HQ_LIB_PATH") or os.path.join(HERE, "libhq.so")
+TRAIN_LIB_PATH = os.environ.get("HQ_TRAIN_LIB_PATH") or os.path.join(HERE, "libhq_train.so")
 
 # enums of include/hq.h
 HQ_OK = 0
@@ -31,6 +32,15 @@ EXPORTS = ["hq_abi_version", "hq_status_string", "hq_code_pitch", "hq_workspace_
            "hq_bmm_workspace_bytes", "hq_bmm_fwd", "hq_bmm_bwd_input", "hq_bmm_bwd_weight",
            "hq_rotated_stat", "hq_cold_start_step", "hq_select_hadamard_k",
            "hq_lss_workspace_bytes", "hq_lss_bwd_weight"]
+# entry points of include/hq_train.h
+TRAIN_EXPORTS = ["hq_train_abi_version", "hq_block_quantize", "hq_block_gemm_workspace_bytes",
+                 "hq_block_gemm", "hq_block_workspace_bytes", "hq_block_linear_fwd",
+                 "hq_block_linear_bwd_input", "hq_block_linear_bwd_weight",
+                 "hq_adamw_scalars_at", "hq_adamw_step"]
+HQ_BLOCK = 128
+HQ_BLOCK_ROWS, HQ_BLOCK_TILES = 0, 1
+HQ_BSCALE_F32, HQ_BSCALE_POW2 = 0, 1
+HQ_SIDE_ROWS, HQ_SIDE_COLS = 0, 1
 HQ_STAT_ABS_SUM, HQ_STAT_QERR, HQ_STAT_LSQ_GRAD = 0, 1, 2
 HQ_MAX_K_CANDIDATES = 16
 HQ_KIND_GEMM, HQ_KIND_ROT_ABSMAX, HQ_KIND_ROT_QUANT, HQ_KIND_ROT_STORE = 0, 1, 2, 3
@@ -66,6 +76,35 @@ class hq_profile_record(ctypes.Structure):
                 ("ms", ctypes.c_double), ("units", ctypes.c_double)]
 
 
+class hq_block_tensor(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("codes_t", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p), ("scales_t", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("ld", ctypes.c_int64),
+                ("ld_t", ctypes.c_int64), ("lds", ctypes.c_int64), ("lds_t", ctypes.c_int64),
+                ("shape", ctypes.c_int32), ("scale", ctypes.c_int32)]
+
+
+class hq_adamw_tensor(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("m", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("m_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("copy", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("weight_decay", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class hq_adamw_config(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("param_dtype", ctypes.c_int32),
+                ("grad_dtype", ctypes.c_int32), ("copy_dtype", ctypes.c_int32),
+                ("state_bits", ctypes.c_int32), ("seed", ctypes.c_uint32),
+                ("reserved", ctypes.c_int32)]
+
+
+class hq_adamw_scalars(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_float), ("step_size", ctypes.c_float),
+                ("inv_sqrt_bias2", ctypes.c_float), ("grad_scale", ctypes.c_float),
+                ("key", ctypes.c_uint32)]
+
+
 class HQError(RuntimeError):
     def __init__(self, status, where=""):
         self.status = status
@@ -74,6 +113,7 @@ class HQError(RuntimeError):
 
 
 _lib = None
+_train_lib = None
 
 
 def load(build_if_missing=True):
@@ -156,6 +196,42 @@ def load(build_if_missing=True):
     lib.hq_profile_records.restype = i32
     lib.hq_profile_records.argtypes = [P(hq_profile_record), i32]
     _lib = lib
+    return lib
+
+
+def load_train():
+    """Load libhq_train.so (after libhq.so, which it links); build both only when it is missing."""
+    global _train_lib
+    if _train_lib is not None:
+        return _train_lib
+    if not os.path.exists(TRAIN_LIB_PATH):
+        from . import build as _build
+        _build.build()
+    load()
+    lib = ctypes.CDLL(TRAIN_LIB_PATH)
+    i32, i64, vp, sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t
+    BT = ctypes.POINTER(hq_block_tensor)
+    for name, restype, argtypes in (
+            ("hq_train_abi_version", i32, []),
+            ("hq_block_quantize", i32, [vp, i32, i64, i64, i32, i32, BT, vp]),
+            ("hq_block_gemm_workspace_bytes", sz, [i64, i64, i64]),
+            ("hq_block_gemm", i32, [BT, i32, BT, i32, vp, i32, i32, vp, sz, vp]),
+            ("hq_block_workspace_bytes", sz, [i64, i64, i64]),
+            ("hq_block_linear_fwd", i32,
+             [vp, i32, i64, i64, i64, BT, i32, vp, i32, BT, vp, sz, vp]),
+            ("hq_block_linear_bwd_input", i32,
+             [vp, i32, i64, i64, i64, BT, i32, vp, i32, BT, vp, sz, vp]),
+            ("hq_block_linear_bwd_weight", i32,
+             [BT, BT, i64, i64, i64, vp, i32, i32, vp, sz, vp]),
+            ("hq_adamw_scalars_at", i32,
+             [ctypes.POINTER(hq_adamw_config), i64, ctypes.c_double,
+              ctypes.POINTER(hq_adamw_scalars)]),
+            ("hq_adamw_step", i32,
+             [ctypes.POINTER(hq_adamw_tensor), i32, ctypes.POINTER(hq_adamw_config),
+              ctypes.POINTER(hq_adamw_scalars), vp, vp])):
+        fn = getattr(lib, name)
+        fn.restype, fn.argtypes = restype, argtypes
+    _train_lib = lib
     return lib
 
 
@@ -278,6 +354,58 @@ def hq_lss_bwd_weight(dy, dy_dtype, saved_x, N, C, D, cfg, budget, uniforms, dw,
 
 def hq_gemm_f8_f32(a, lda, b_t, ldb, c, M, N, K, stream):
     return load().hq_gemm_f8_f32(a, lda, b_t, ldb, c, M, N, K, stream)
+
+
+# ------------------------------------------------ entry points of include/hq_train.h
+def hq_train_abi_version():
+    return load_train().hq_train_abi_version()
+
+
+def hq_block_quantize(src, src_dtype, rows, cols, shape, scale, out, stream):
+    return load_train().hq_block_quantize(src, src_dtype, rows, cols, shape, scale, _ref(out),
+                                          stream)
+
+
+def hq_block_gemm_workspace_bytes(M, N, K):
+    return load_train().hq_block_gemm_workspace_bytes(M, N, K)
+
+
+def hq_block_gemm(a, a_side, b, b_side, c, c_dtype, accumulate, ws, ws_bytes, stream):
+    return load_train().hq_block_gemm(_ref(a), a_side, _ref(b), b_side, c, c_dtype, accumulate,
+                                      ws, ws_bytes, stream)
+
+
+def hq_block_workspace_bytes(N, C, D):
+    return load_train().hq_block_workspace_bytes(N, C, D)
+
+
+def hq_block_linear_fwd(x, x_dtype, N, C, D, w, scale, y, y_dtype, save_x, ws, ws_bytes, stream):
+    return load_train().hq_block_linear_fwd(x, x_dtype, N, C, D, _ref(w), scale, y, y_dtype,
+                                            _ref(save_x), ws, ws_bytes, stream)
+
+
+def hq_block_linear_bwd_input(dy, dy_dtype, N, C, D, w, scale, dx, dx_dtype, save_g, ws, ws_bytes,
+                              stream):
+    return load_train().hq_block_linear_bwd_input(dy, dy_dtype, N, C, D, _ref(w), scale, dx,
+                                                  dx_dtype, _ref(save_g), ws, ws_bytes, stream)
+
+
+def hq_block_linear_bwd_weight(saved_g, saved_x, N, C, D, dw, dw_dtype, accumulate, ws, ws_bytes,
+                               stream):
+    return load_train().hq_block_linear_bwd_weight(_ref(saved_g), _ref(saved_x), N, C, D, dw,
+                                                   dw_dtype, accumulate, ws, ws_bytes, stream)
+
+
+def hq_adamw_scalars_at(cfg, step, grad_scale, out):
+    """out: an hq_adamw_scalars on the host."""
+    return load_train().hq_adamw_scalars_at(_ref(cfg), step, grad_scale, _ref(out))
+
+
+def hq_adamw_step(tensors, count, cfg, host_scalars, device_scalars, stream):
+    """tensors: a ctypes array of hq_adamw_tensor; host_scalars: an hq_adamw_scalars or None;
+    device_scalars: a device pointer or None."""
+    return load_train().hq_adamw_step(tensors, count, _ref(cfg), _ref(host_scalars),
+                                      device_scalars, stream)
 
 
 def hq_profile_start(kind_mask):

@@ -1,4 +1,5 @@
-"""Build libhq.so (the gfx950 HIP kernels and the C ABI of include/hq.h) in-tree with hipcc."""
+"""Build libhq.so (the gfx950 HIP kernels and the C ABI of include/hq.h) and libhq_train.so (those
+of include/hq_train.h) in-tree with hipcc."""
 import os
 import subprocess
 import sys
@@ -10,6 +11,9 @@ LIB = os.path.join(HERE, "libhq.so")
 
 SOURCES = ["hq_rotate.hip", "hq_prologue.hip", "hq_gemm.hip", "hq_static.hip", "hq_lss.hip", "hq_api.cpp",
            "hq_profile.cpp"]
+# the operators of include/hq_train.h, a library of their own that links libhq.so
+TRAIN_LIB = os.path.join(HERE, "libhq_train.so")
+TRAIN_SOURCES = ["hq_block.hip", "hq_block_gemm.hip", "hq_adamw.hip", "hq_train_api.cpp"]
 
 # -packed-fp32-ops: hipcc forms packed fp32 ops from plain float code; keep them out.
 HIP_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
@@ -18,10 +22,22 @@ HIP_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
              "-I" + os.path.join(ROOT, "include")]
 
 
+TRAIN_LINK = ["-L" + HERE, "-lhq", "-Wl,-rpath,$ORIGIN"]
+
+
+def link(lib, objs, verbose=False, extra=()):
+    cmd = (["hipcc", "--offload-arch=gfx950", "-shared", "-fPIC"] + objs + list(extra) +
+           ["-o", lib + ".tmp"])
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(lib + ".tmp", lib)
+
+
 def build(verbose=False, jobs=None):
     objs = []
     procs = []
-    for src in SOURCES:
+    for src in SOURCES + TRAIN_SOURCES:
         obj = os.path.join(CSRC, src + ".o")
         lang = ["-x", "hip"] if src.endswith(".hip") else []
         cmd = ["hipcc"] + HIP_FLAGS + lang + ["-c", os.path.join(CSRC, src), "-o", obj]
@@ -32,11 +48,9 @@ def build(verbose=False, jobs=None):
     for cmd, p in procs:
         if p.wait() != 0:
             raise RuntimeError("compile failed: " + " ".join(cmd))
-    cmd = ["hipcc", "--offload-arch=gfx950", "-shared", "-fPIC"] + objs + ["-o", LIB + ".tmp"]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
-    os.replace(LIB + ".tmp", LIB)
+    n = len(SOURCES)
+    link(LIB, objs[:n], verbose)
+    link(TRAIN_LIB, objs[n:], verbose, TRAIN_LINK)
     for o in objs:
         os.remove(o)
     return LIB

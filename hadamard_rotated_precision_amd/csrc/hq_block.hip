@@ -1,0 +1,203 @@
+// hq_block.hip — block-scaled FP8 quantizer: E4M3 codes with one scale for each 1 x 128 (ROWS) or
+// 128 x 128 (TILES) block, row-major and transposed codes from one read of the source.
+//
+// For a block with largest magnitude a: s = fp32(a / 448), at least 2^-126 (POW2: rounded up to a
+// power of two), r = fp32(1 / s), code = E4M3(v r) to nearest even. 448 is the format's largest
+// value. The maxima are taken on the bit patterns of |v| as integers: they order like the
+// magnitudes, and an infinity or a NaN comes out on top instead of being skipped.
+//
+// What bounds it: bytes. R x C elements of e bytes are read once, R C bytes of codes are written
+// for each layout.
+//
+// One workgroup of 256 threads takes a 128 x 128 tile, which holds whole blocks of either
+// direction: thread t has columns 8 (t % 16) + [0, 8) of rows 8 (t / 16) + [0, 8) in registers, so
+// the source is read once (16 lanes cover 256 contiguous bytes of a 16-bit row), the row maxima
+// are a reduction over 16 lanes, the column maxima over the eight rows in registers, four lanes
+// and four waves (LDS), and a column's eight codes of a thread pack into two dwords. Those go to
+// LDS and leave as 16-byte pieces of the transposed rows.
+#include "hq_device.hpp"
+#include "hq_launch.hpp"
+#include "hq_train_internal.hpp"
+
+namespace hq {
+
+struct BlockQuantArgs {
+  const void* src;
+  int64_t rows, cols;
+  uint8_t* codes;
+  int64_t ld;
+  uint8_t* codes_t;
+  int64_t ld_t;
+  float* scales;
+  int64_t lds;
+  float* scales_t;
+  int64_t lds_t;
+  int tiles_c;
+  int pow2;
+  int vec;   // rows start on 16-byte boundaries and hold whole groups of eight elements
+};
+
+// The scale of a block whose largest magnitude has the bit pattern `a`, and r = 1 / s. A NaN or
+// infinity: s = NaN, r = 0.
+__device__ inline void block_scale(uint32_t a, bool pow2, float& s, float& r) {
+  s = __uint_as_float(a) / 448.0f;   // correctly rounded
+  if (pow2) s = __uint_as_float((__float_as_uint(s) + 0x7FFFFFu) & 0x7F800000u);
+  s = fmaxf(s, 1.17549435e-38f);     // 2^-126: 1 / s stays finite
+  r = 1.0f / s;
+  if (a == 0u) s = 0.0f, r = 0.0f;
+  if (a >= 0x7F800000u) s = __uint_as_float(0x7FC00000u), r = 0.0f;
+}
+
+// Eight elements from element i of the source (n of them valid).
+template <class T>
+__device__ inline void load8(const void* src, int64_t i, int n, bool vec, float (&v)[8]) {
+  if (vec && n >= 8) {
+    const char* p = static_cast<const char*>(src) + i * T::bytes;
+    if constexpr (T::bytes == 4) {
+      const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else {
+      const uint4 q = *reinterpret_cast<const uint4*>(p);
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[2 * j] = T::from_bits(static_cast<uint16_t>(w[j] & 0xFFFFu));
+        v[2 * j + 1] = T::from_bits(static_cast<uint16_t>(w[j] >> 16));
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = j < n ? T::load(src, i + j) : 0.0f;
+  }
+}
+
+__device__ inline uint32_t mag(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+__device__ inline uint32_t shfl_max(uint32_t x, int m) {
+  return max(x, static_cast<uint32_t>(__shfl_xor(static_cast<int>(x), m, 64)));
+}
+
+template <class T, bool TILES>
+__global__ __launch_bounds__(256) void block_quant_kernel(BlockQuantArgs g) {
+  constexpr int TP = 144;   // LDS pitch of a transposed code row
+  __shared__ uint32_t cmax[4][128];
+  __shared__ __attribute__((aligned(16))) uint8_t turned[128 * TP];
+  const int t = threadIdx.x, cg = t & 15, rg = t >> 4, wave = t >> 6;
+  const int tr = blockIdx.x / g.tiles_c, tc = blockIdx.x % g.tiles_c;
+  const int64_t r0 = static_cast<int64_t>(tr) * 128, c0 = static_cast<int64_t>(tc) * 128;
+  const int64_t row0 = r0 + 8 * rg, col0 = c0 + 8 * cg;
+  const int ncol = static_cast<int>(min<int64_t>(max<int64_t>(g.cols - col0, 0), 8));
+
+  float v[8][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    load8<T>(g.src, (row0 + i) * g.cols + col0, row0 + i < g.rows ? ncol : 0, g.vec, v[i]);
+
+  uint32_t rm[8], cm[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    rm[i] = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) rm[i] = max(rm[i], mag(v[i][j]));
+  }
+  float sr[8], rr[8];
+  if constexpr (TILES) {
+    uint32_t a = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a = max(a, rm[i]);
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) a = shfl_max(a, m);
+    if ((t & 63) == 0) cmax[wave][0] = a;
+    __syncthreads();
+    a = max(max(cmax[0][0], cmax[1][0]), max(cmax[2][0], cmax[3][0]));
+    float s, r;
+    block_scale(a, g.pow2, s, r);
+    if (t == 0) g.scales[tr * g.lds + tc] = s;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sr[i] = s, rr[i] = r;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+#pragma unroll
+      for (int m = 1; m < 16; m <<= 1) rm[i] = shfl_max(rm[i], m);
+      block_scale(rm[i], g.pow2, sr[i], rr[i]);
+    }
+  }
+
+  if (g.codes) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint2 q;
+      q.x = e4m3_pack4(v[i][0], v[i][1], v[i][2], v[i][3], rr[i]);
+      q.y = e4m3_pack4(v[i][4], v[i][5], v[i][6], v[i][7], rr[i]);
+      if (!(sr[i] == sr[i])) q = {0u, 0u};
+      // zeros up to the next multiple of 16 columns, which the pitch covers
+      if (row0 + i < g.rows && col0 < ((g.cols + 15) & ~int64_t{15}))
+        *reinterpret_cast<uint2*>(g.codes + (row0 + i) * g.ld + col0) = q;
+      if (!TILES && cg == 0 && row0 + i < g.rows) g.scales[tc * g.lds + row0 + i] = sr[i];
+    }
+  }
+  if (!g.codes_t) return;
+
+  float sc[8], rc[8];
+  if constexpr (TILES) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sc[j] = sr[0], rc[j] = rr[0];
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      cm[j] = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) cm[j] = max(cm[j], mag(v[i][j]));
+      cm[j] = shfl_max(shfl_max(cm[j], 16), 32);
+      if ((t & 48) == 0) cmax[wave][8 * cg + j] = cm[j];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = 8 * cg + j;
+      block_scale(max(max(cmax[0][c], cmax[1][c]), max(cmax[2][c], cmax[3][c])), g.pow2, sc[j], rc[j]);
+      if (rg == 0 && j < ncol) g.scales_t[tr * g.lds_t + col0 + j] = sc[j];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    uint2 q;
+    q.x = e4m3_pack4(v[0][j], v[1][j], v[2][j], v[3][j], rc[j]);
+    q.y = e4m3_pack4(v[4][j], v[5][j], v[6][j], v[7][j], rc[j]);
+    if (!(sc[j] == sc[j])) q = {0u, 0u};
+    *reinterpret_cast<uint2*>(&turned[(8 * cg + j) * TP + 8 * rg]) = q;
+  }
+  __syncthreads();
+  // 8 lanes cover the 128 codes of a transposed row
+  const int64_t rows16 = (g.rows + 15) & ~int64_t{15};
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    const int c = (t >> 3) + 32 * p, part = 16 * (t & 7);
+    if (c0 + c < g.cols && r0 + part < rows16)
+      *reinterpret_cast<uint4*>(g.codes_t + (c0 + c) * g.ld_t + r0 + part) =
+          *reinterpret_cast<const uint4*>(&turned[c * TP + part]);
+  }
+}
+
+hipError_t block_quant_pass(const BlockQuantPass& p, hipStream_t st) {
+  const int64_t tiles_r = (p.rows + 127) / 128, tiles_c = (p.cols + 127) / 128;
+  BlockQuantArgs a{p.src, p.rows, p.cols, p.codes, p.ld, p.codes_t, p.ld_t, p.scales, p.lds,
+                   p.scales_t, p.lds_t, static_cast<int>(tiles_c), p.pow2, p.cols % 8 == 0};
+  const int bytes = p.in_dt == DT_F32 ? 4 : 2;
+  const double units = static_cast<double>(p.rows) * p.cols * (bytes + (p.codes != nullptr) + (p.codes_t != nullptr));
+  const int tok = prof_open(K_ROT_QUANT, units);
+  const dim3 grid(static_cast<unsigned>(tiles_r * tiles_c)), block(256);
+#define HQ_Q(T) \
+  return p.tiles ? launch_k(block_quant_kernel<T, true>, grid, block, st, tok, a) \
+                 : launch_k(block_quant_kernel<T, false>, grid, block, st, tok, a)
+  switch (p.in_dt) {
+    case DT_F32: HQ_Q(F32);
+    case DT_F16: HQ_Q(F16);
+    case DT_BF16: HQ_Q(BF16);
+  }
+#undef HQ_Q
+  return hipErrorInvalidValue;
+}
+
+}  // namespace hq

@@ -172,3 +172,320 @@ class LssGrad:
         h = self.stats.cpu().numpy()
         f = h.view(np.float32)
         return int(h[0]), np.float32(f[1]), np.float32(f[2]), np.float32(f[3])
+
+
+# ------------------------------------------------------------------ block-scaled FP8, AdamW
+def _blocks(n):
+    return (n + B.HQ_BLOCK - 1) // B.HQ_BLOCK
+
+
+def _on(t):
+    """The tensor's device as the current one (a call launches on the current device)."""
+    return torch.cuda.device(t.device)
+
+
+def _stream_of(t, stream):
+    return (torch.cuda.current_stream(t.device) if stream is None else stream).cuda_stream
+
+
+def _check_matrix(t, rows, cols, name, device=None):
+    """A call reads rows x cols contiguous elements at the tensor's address."""
+    if tuple(t.shape) != (rows, cols):
+        raise ValueError("%s has shape %s, not %s" % (name, tuple(t.shape), (rows, cols)))
+    if t.dtype not in HQ_DT:
+        raise ValueError("%s has dtype %s: fp32, fp16 or bf16 is needed" % (name, t.dtype))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    if device is not None and t.device != device:
+        raise ValueError("%s is on %s, not on %s" % (name, t.device, device))
+
+
+class BlockTensor:
+    """Caller-owned storage of a block-scaled FP8 matrix (hq_block_tensor): E4M3 codes
+    (rows x pitch), transposed codes (cols x pitch) and their scales. ROWS blocks (1 x 128) have
+    scales (column blocks x rows) and scales_t (row blocks x cols); TILES (128 x 128) have one
+    scales (row blocks x column blocks) for both layouts."""
+
+    def __init__(self, rows, cols, shape=B.HQ_BLOCK_ROWS, scale=B.HQ_BSCALE_F32, codes=True,
+                 codes_t=True, device="cuda"):
+        def new(wanted, *size, dtype=torch.float32):
+            return torch.empty(size, dtype=dtype, device=device) if wanted else None
+
+        rows_kind = shape == B.HQ_BLOCK_ROWS
+        self._set(rows, cols, shape, scale,
+                  new(codes, rows, pitch16(cols), dtype=torch.uint8),
+                  new(codes_t, cols, pitch16(rows), dtype=torch.uint8),
+                  new(codes, _blocks(cols), rows) if rows_kind
+                  else new(True, _blocks(rows), _blocks(cols)),
+                  new(codes_t, _blocks(rows), cols) if rows_kind else None)
+
+    def _set(self, rows, cols, shape, scale, codes, codes_t, scales, scales_t):
+        self.rows, self.cols, self.shape, self.scale = rows, cols, shape, scale
+        self.codes, self.codes_t, self.scales, self.scales_t = codes, codes_t, scales, scales_t
+        self.device = next(t for t in (codes, codes_t, scales) if t is not None).device
+        st = self.st = B.hq_block_tensor()
+        st.codes, st.codes_t = ptr(codes), ptr(codes_t)
+        st.scales, st.scales_t = ptr(scales), ptr(scales_t)
+        st.rows, st.cols, st.shape, st.scale = rows, cols, shape, scale
+        st.ld = 0 if codes is None else codes.stride(0)
+        st.ld_t = 0 if codes_t is None else codes_t.stride(0)
+        st.lds = 0 if scales is None else scales.stride(0)
+        st.lds_t = 0 if scales_t is None else scales_t.stride(0)
+
+    @classmethod
+    def wrap(cls, codes, scales, rows, cols, shape=B.HQ_BLOCK_TILES, scale=B.HQ_BSCALE_F32,
+             codes_t=None, scales_t=None):
+        """A matrix whose codes exist already (weights of a checkpoint): codes (rows x pitch, the
+        bytes from cols to the next multiple of 16 zero), scales as above. The buffers are used
+        as they are. Checks their shapes and, once, on the host, that scales of kind POW2 are
+        powers of two."""
+        self = cls.__new__(cls)
+        parts = [("codes", codes, rows, cols, torch.uint8),
+                 ("codes_t", codes_t, cols, rows, torch.uint8)]
+        if shape == B.HQ_BLOCK_TILES:
+            parts += [("scales", scales, _blocks(rows), _blocks(cols), torch.float32)]
+        else:
+            parts += [("scales", scales, _blocks(cols), rows, torch.float32),
+                      ("scales_t", scales_t, _blocks(rows), cols, torch.float32)]
+        for name, t, r, c, dtype in parts:
+            if t is None:
+                continue
+            if t.dtype != dtype or t.dim() != 2 or t.shape[0] != r or t.shape[1] < c:
+                raise ValueError("%s must be a %s tensor of at least %d x %d" % (name, dtype, r, c))
+            if t.stride(1) != 1 and t.shape[1] > 1:
+                raise ValueError("%s must have contiguous rows" % name)
+            if t.device != codes.device:
+                raise ValueError("%s is on %s, not on %s" % (name, t.device, codes.device))
+        for t in (scales, scales_t):
+            if scale == B.HQ_BSCALE_POW2 and t is not None and t.numel():
+                mantissa, _ = torch.frexp(t)
+                if not bool(((mantissa == 0.5) | (t == 0) | t.isnan()).all()):
+                    raise ValueError("scales of kind POW2 must be powers of two")
+        self._set(rows, cols, shape, scale, codes, codes_t, scales, scales_t)
+        return self
+
+    def quantize(self, src, stream=None):
+        """hq_block_quantize of src (rows x cols, contiguous) into these buffers."""
+        _check_matrix(src, self.rows, self.cols, "src", self.device)
+        with _on(src):
+            B.check(B.hq_block_quantize(ptr(src), HQ_DT[src.dtype], self.rows, self.cols,
+                                        self.shape, self.scale, self.st, _stream_of(src, stream)),
+                    "hq_block_quantize")
+        return self
+
+    def codes_view(self):
+        return None if self.codes is None else self.codes[:, :self.cols]
+
+    def codes_t_view(self):
+        return None if self.codes_t is None else self.codes_t[:, :self.rows]
+
+
+class _Workspace:
+    """Scratch of a layer's calls, and its size."""
+
+    def __init__(self, nbytes, device):
+        self.nbytes = nbytes
+        self.buf = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+
+
+def block_gemm(a, b, c, a_side=B.HQ_SIDE_ROWS, b_side=B.HQ_SIDE_ROWS, accumulate=False, ws=None,
+               stream=None):
+    """hq_block_gemm: c (+)= a b^T over BlockTensors (HQ_SIDE_COLS reads the transposed codes).
+    ws: a uint8 tensor of hq_block_gemm_workspace_bytes, allocated here when missing."""
+    M, K = (a.rows, a.cols) if a_side == B.HQ_SIDE_ROWS else (a.cols, a.rows)
+    N = b.rows if b_side == B.HQ_SIDE_ROWS else b.cols
+    _check_matrix(c, M, N, "c", a.device)
+    if b.device != a.device:
+        raise ValueError("b is on %s, not on %s" % (b.device, a.device))
+    with _on(c):
+        if ws is None:
+            ws = torch.empty(max(B.hq_block_gemm_workspace_bytes(M, N, K), 16), dtype=torch.uint8,
+                             device=c.device)
+            if stream is not None:
+                ws.record_stream(stream)
+        B.check(B.hq_block_gemm(a.st, a_side, b.st, b_side, ptr(c), HQ_DT[c.dtype],
+                                int(accumulate), ptr(ws), ws.numel(), _stream_of(c, stream)),
+                "hq_block_gemm")
+
+
+class BlockLayer:
+    """Buffers for one linear layer (N tokens, C in, D out) in block-scaled FP8 and its calls.
+
+    train=True keeps Q(X) and Q(dY) in both layouts for the weight gradient; train=False is the
+    serving form (forward alone, nothing saved). weight: a BlockTensor that the layer reads (D x C,
+    for instance BlockTensor.wrap of a checkpoint's codes); without it set_weight quantizes W into
+    TILES of the layer's own."""
+
+    def __init__(self, N, C, D, scale=B.HQ_BSCALE_F32, weight=None, train=True, device="cuda"):
+        self.N, self.C, self.D, self.scale, self.train = N, C, D, scale, train
+        if weight is not None:
+            if (weight.rows, weight.cols) != (D, C):
+                raise ValueError("weight is %d x %d, not %d x %d" % (weight.rows, weight.cols, D, C))
+            device = weight.device
+        self.qw = weight or BlockTensor(D, C, shape=B.HQ_BLOCK_TILES, scale=scale, codes_t=train,
+                                        device=device)
+        self.device = self.qw.device
+        self.qx = BlockTensor(N, C, scale=scale, device=device) if train else None
+        self.qg = BlockTensor(N, D, scale=scale, device=device) if train else None
+        self.ws_bytes = B.hq_block_workspace_bytes(N, C, D)
+        self.ws = torch.empty(max(self.ws_bytes, 16), dtype=torch.uint8, device=device)
+
+    def set_weight(self, w, stream=None):
+        self.qw.quantize(w, stream)
+
+    def fwd(self, x, y, stream=None):
+        _check_matrix(x, self.N, self.C, "x", self.device)
+        _check_matrix(y, self.N, self.D, "y", self.device)
+        with _on(x):
+            B.check(B.hq_block_linear_fwd(
+                ptr(x), HQ_DT[x.dtype], self.N, self.C, self.D, self.qw.st, self.scale, ptr(y),
+                HQ_DT[y.dtype], None if self.qx is None else self.qx.st, ptr(self.ws),
+                self.ws_bytes, _stream_of(x, stream)), "hq_block_linear_fwd")
+
+    def bwd_input(self, dy, dx, stream=None):
+        _check_matrix(dy, self.N, self.D, "dy", self.device)
+        _check_matrix(dx, self.N, self.C, "dx", self.device)
+        with _on(dy):
+            B.check(B.hq_block_linear_bwd_input(
+                ptr(dy), HQ_DT[dy.dtype], self.N, self.C, self.D, self.qw.st, self.scale, ptr(dx),
+                HQ_DT[dx.dtype], None if self.qg is None else self.qg.st, ptr(self.ws),
+                self.ws_bytes, _stream_of(dy, stream)), "hq_block_linear_bwd_input")
+
+    def bwd_weight(self, dw, accumulate=False, stream=None):
+        """From the codes that fwd and bwd_input saved."""
+        if not self.train:
+            raise ValueError("a layer made with train=False saves nothing for the weight gradient")
+        _check_matrix(dw, self.D, self.C, "dw", self.device)
+        with _on(dw):
+            B.check(B.hq_block_linear_bwd_weight(
+                self.qg.st, self.qx.st, self.N, self.C, self.D, ptr(dw), HQ_DT[dw.dtype],
+                int(accumulate), ptr(self.ws), self.ws_bytes, _stream_of(dw, stream)),
+                "hq_block_linear_bwd_weight")
+
+
+class AdamW:
+    """AdamW over a list of parameter tensors of one dtype and device (hq_adamw_step).
+
+    state_bits: 32 (fp32 states) or 8 (E4M3 codes with a scale for each 128 elements).
+    weight_decay: one number, or one for each tensor. copies: tensors of one dtype that receive
+    the updated parameters (the low-precision weights of the next forward). states: dicts of m, v
+    (and m_scales, v_scales for 8 bits) to go on from, used in place; zeros without it.
+    steps_done: steps taken before.
+
+    step(grads) takes the next step. Under HIP graph capture a step has to read its scalars from
+    device memory: step(grads, captured=True) launches with `device_scalars`, and
+    advance(grad_scale) writes the next step's there before each replay."""
+
+    def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01,
+                 state_bits=32, copies=None, states=None, seed=0, steps_done=0):
+        params = list(params)
+        if not params:
+            raise ValueError("no parameters")
+        decay = ([float(weight_decay)] * len(params) if isinstance(weight_decay, (int, float))
+                 else [float(w) for w in weight_decay])
+        if len(decay) != len(params):
+            raise ValueError("weight_decay needs one number for each tensor")
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits is 8 or 32")
+        self.params, self.device, self.step_count = params, params[0].device, int(steps_done)
+        self.state_bits = state_bits
+        self._check("parameter", params, params[0].dtype)
+        self.copies = None if copies is None else list(copies)
+        if self.copies is not None:
+            self._check("copy", self.copies, self.copies[0].dtype if self.copies else None)
+        self.states = [self._zeros(p) for p in params] if states is None else list(states)
+        if len(self.states) != len(params):
+            raise ValueError("one state for each parameter is needed")
+        c = self.cfg = B.hq_adamw_config()
+        c.lr, (c.beta1, c.beta2), c.eps = lr, betas, eps
+        c.param_dtype = HQ_DT[params[0].dtype]
+        c.copy_dtype = HQ_DT[self.copies[0].dtype] if self.copies else c.param_dtype
+        c.grad_dtype, c.state_bits, c.seed = c.param_dtype, state_bits, seed & 0xFFFFFFFF
+        self._scalars = B.hq_adamw_scalars()
+        self._device_scalars = None
+        self._table = (B.hq_adamw_tensor * len(params))()
+        for i, (t, p, s) in enumerate(zip(self._table, params, self.states)):
+            self._check_state(s, p.numel())
+            t.p, t.n, t.weight_decay = ptr(p), p.numel(), decay[i]
+            t.m, t.v = ptr(s["m"]), ptr(s["v"])
+            t.m_scales, t.v_scales = ptr(s.get("m_scales")), ptr(s.get("v_scales"))
+            t.copy = ptr(self.copies[i]) if self.copies else None
+
+    def _zeros(self, p):
+        n, dev = p.numel(), p.device
+        if self.state_bits == 32:
+            return {k: torch.zeros(n, dtype=torch.float32, device=dev) for k in ("m", "v")}
+        s = {k: torch.zeros(n, dtype=torch.uint8, device=dev) for k in ("m", "v")}
+        s.update({k + "_scales": torch.zeros(_blocks(n), dtype=torch.float32, device=dev)
+                  for k in ("m", "v")})
+        return s
+
+    def _check(self, what, tensors, dtype):
+        if len(tensors) != len(self.params):
+            raise ValueError("%d tensors of kind %s for %d parameters"
+                             % (len(tensors), what, len(self.params)))
+        for i, (t, p) in enumerate(zip(tensors, self.params)):
+            if t.numel() != p.numel() or not t.is_contiguous() or t.device != self.device:
+                raise ValueError("%s %d must be contiguous, on %s, with %d elements"
+                                 % (what, i, self.device, p.numel()))
+            if t.dtype != dtype or t.dtype not in HQ_DT:
+                raise ValueError("%s %d has dtype %s: one of fp32, fp16, bf16 for all is needed"
+                                 % (what, i, t.dtype))
+
+    def _check_state(self, s, n):
+        eight = self.state_bits == 8
+        parts = [(k, n, torch.uint8 if eight else torch.float32) for k in ("m", "v")]
+        if eight:
+            parts += [(k, _blocks(n), torch.float32) for k in ("m_scales", "v_scales")]
+        for k, size, dtype in parts:
+            t = s.get(k)
+            if (t is None or t.numel() != size or t.dtype != dtype or not t.is_contiguous()
+                    or t.device != self.device):
+                raise ValueError("state %s must be a contiguous %s tensor of %d elements on %s"
+                                 % (k, dtype, size, self.device))
+
+    @property
+    def device_scalars(self):
+        """The device copy of the step's scalars that captured steps read (five 32-bit words: lr,
+        step_size, inv_sqrt_bias2, grad_scale as floats, then the key)."""
+        if self._device_scalars is None:
+            self._device_scalars = torch.zeros(5, dtype=torch.float32, device=self.device)
+        return self._device_scalars
+
+    def set_lr(self, lr):
+        self.cfg.lr = lr
+
+    def advance(self, grad_scale=1.0):
+        """Count one step and write its scalars to device_scalars (in stream order)."""
+        s = self._scalars
+        B.check(B.hq_adamw_scalars_at(self.cfg, self.step_count + 1, grad_scale, s),
+                "hq_adamw_scalars_at")
+        self.step_count += 1
+        host = torch.frombuffer(bytearray(bytes(s)), dtype=torch.float32)
+        self.device_scalars.copy_(host)
+
+    def step(self, grads, grad_scale=1.0, captured=False, stream=None):
+        """One step with one gradient for each parameter (one dtype for all)."""
+        if len(grads) != len(self.params):
+            raise ValueError("%d gradients for %d parameters" % (len(grads), len(self.params)))
+        for i, g in enumerate(grads):
+            t = self._table[i]
+            if g.numel() != t.n or not g.is_contiguous() or g.device != self.device:
+                raise ValueError("gradient %d must be contiguous, on %s, with %d elements"
+                                 % (i, self.device, t.n))
+            if g.dtype not in HQ_DT or g.dtype != grads[0].dtype:
+                raise ValueError("gradient %d has dtype %s" % (i, g.dtype))
+            t.grad = g.data_ptr()
+        self.cfg.grad_dtype = HQ_DT[grads[0].dtype]
+        if captured:
+            scalars = None
+        else:
+            scalars = self._scalars
+            B.check(B.hq_adamw_scalars_at(self.cfg, self.step_count + 1, grad_scale, scalars),
+                    "hq_adamw_scalars_at")
+        with _on(self.params[0]):
+            B.check(B.hq_adamw_step(self._table, len(self.params), self.cfg, scalars,
+                                    ptr(self.device_scalars) if captured else None,
+                                    _stream_of(self.params[0], stream)), "hq_adamw_step")
+        if not captured:
+            self.step_count += 1

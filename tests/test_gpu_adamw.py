@@ -1,0 +1,286 @@
+"""The AdamW step against the formula in 64 bits: 32-bit states, 8-bit states and their rounding,
+many tensors, captured steps, refusals, and a whole training step of a block-scaled layer."""
+import math
+
+import pytest
+import torch
+
+import train_testlib as R
+from hadamard_rotated_precision_amd import binding as B
+from hadamard_rotated_precision_amd import tensors as T
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+U = 2.0 ** -24
+HYPER = dict(lr=3e-3, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.1)
+
+
+def gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return g
+
+
+def randn(g, n, scale=1.0):
+    return torch.randn(n, generator=g, device=DEV) * scale
+
+
+def formula(p, g, m, v, step, grad_scale=1.0, lr=3e-3, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.1):
+    """(p, m, v, and bounds of fp32 errors) from 64-bit inputs. fp32: each constant and operation
+    is off by at most U of its result. m: two products of rounded constants and a sum, under 5 U of
+    the terms' magnitudes; v: under 7 U; den: sqrt halves v's, three more roundings, 8 U; the update
+    adds a quotient, a product and the constant, p its own product, constant and difference."""
+    b1, b2 = betas
+    g = g * grad_scale
+    size = (b1 * m).abs() + ((1 - b1) * g).abs()
+    m = b1 * m + (1 - b1) * g
+    v = b2 * v + (1 - b2) * g * g
+    den = v.sqrt() / math.sqrt(1 - b2 ** step) + eps
+    rate = lr / (1 - b1 ** step)
+    new = p * (1 - lr * weight_decay) - rate * m / den
+    bound = 4 * U * p.abs() + U * new.abs() + rate / den * (6 * U * size + 13 * U * m.abs())
+    return new, m, v, (bound, 6 * U * size, 8 * U * v)
+
+
+def stored(x64, bound, dtype):
+    """Bound of x rounded to dtype."""
+    tiny = 2.0 ** -25 if dtype == torch.float16 else 2.0 ** -126
+    return bound + R.HALF_STEP[dtype] * (x64.abs() + bound) + tiny
+
+
+@pytest.mark.parametrize("n", [1, 2, 7, 8, 9, 127, 128, 129, 2047, 2048, 2049, 100003])
+@pytest.mark.parametrize("pdt,gdt,cdt", [
+    (torch.float32, torch.float32, None), (torch.float32, torch.bfloat16, torch.bfloat16),
+    (torch.bfloat16, torch.bfloat16, None), (torch.float16, torch.float32, torch.float16),
+    (torch.float32, torch.float16, torch.float32)])
+def test_step_in_32_bits(n, pdt, gdt, cdt):
+    g = gen(n)
+    p, grad = randn(g, n, 0.02).to(pdt), randn(g, n, 1e-3).to(gdt)
+    st = {"m": randn(g, n, 1e-3), "v": randn(g, n, 1e-3).square()}
+    copy = None if cdt is None else torch.zeros(n, dtype=cdt, device=DEV)
+    want, m, v, (bp, bm, bv) = formula(p.double(), grad.double(), st["m"].double(),
+                                       st["v"].double(), 6, 0.5)
+    opt = T.AdamW([p], states=[st], steps_done=5, copies=None if copy is None else [copy], **HYPER)
+    opt.step([grad], grad_scale=0.5)
+    R.assert_within(p, want, stored(want, bp, pdt), "p")
+    if copy is not None:
+        R.assert_within(copy, want, stored(want, bp, cdt), "copy")
+    R.assert_within(st["m"], m, bm + 2.0 ** -149, "m")
+    R.assert_within(st["v"], v, bv + 2.0 ** -149, "v")
+
+
+def neighbours(x):
+    """The grid values around x >= 0 (fp64): low <= x <= high."""
+    _, e = torch.frexp(x)
+    ulp = torch.exp2((e - 1).clamp_min(-6).double() - 3.0)
+    low = torch.floor(x / ulp) * ulp
+    return low, low + ulp
+
+
+def eight_bit_values(st, n):
+    at = torch.arange(n, device=DEV) // 128
+    m = st["m"].view(R.E4M3).double() * st["m_scales"].double()[at]
+    return m, (st["v"].view(R.E4M3).double() * st["v_scales"].double()[at]).square()
+
+
+@pytest.mark.parametrize("n", [1, 5, 8, 127, 128, 130, 2048, 2050, 70001])
+def test_step_in_8_bits(n):
+    """p as with 32-bit states of the same values; new states on a neighbour of the exact value."""
+    g = gen(n)
+    p, grad = randn(g, n, 0.02), (randn(g, n, 1e-3) * torch.exp(randn(g, n, 2.0)))
+    opt = T.AdamW([p], state_bits=8, seed=5, **HYPER)
+    st = opt.states[0]
+    for step in range(1, 4):
+        m0, v0 = eight_bit_values(st, n)
+        want, m, v, (bp, bm, bv) = formula(p.double(), grad.double(), m0, v0, step)
+        opt.step([grad])
+        R.assert_within(p, want, stored(want, bp, torch.float32), "p")
+        for name, exact, bound in (("m", m, bm), ("v", v.sqrt(), bv / v.sqrt().clamp_min(1e-30))):
+            at = torch.arange(n, device=DEV) // 128
+            s = st[name + "_scales"].double()
+            a = R.block_max(exact.view(1, -1), 1, 128).view(-1)
+            assert ((s - a / 448).abs() <= 16 * U * a / 448 + 2.0 ** -126).all()
+            q = st[name].view(R.E4M3).double()
+            assert (q * exact >= 0).all()
+            x, q = exact.abs() / s[at].clamp_min(1e-300), q.abs()
+            off = bound / s[at].clamp_min(1e-300) + 16 * U * x   # fp32 errors of x
+            low, high = neighbours((x - off).clamp_min(0))[0], neighbours((x + off).clamp(max=448))[1]
+            ok = (q >= low) & (q <= high)
+            if name == "v":
+                ok |= (q == 2.0 ** -9) & (v > 0) & (x < 2.0 ** -9)
+                assert (q[v > 0] > 0).all()
+            assert ok.all(), (name, int((~ok).sum()))
+        grad = randn(g, n, 1e-3)
+
+
+def test_8_bit_rounding_is_unbiased():
+    """Many elements of one value: the mean of m, and of v, over the elements is the value itself,
+    within five standard deviations (a rounded value differs by at most one step)."""
+    n = 128 * 2000
+    for value in (0.3, 0.011, 3.1e-4):   # steps of normal codes, and of the subnormal ones
+        grad = torch.full((n,), value, device=DEV)
+        grad[::128] = 1.0      # the block's largest
+        p = torch.zeros(n, device=DEV)
+        opt = T.AdamW([p], lr=1e-3, betas=(0.0, 0.0), state_bits=8, seed=1)   # m = g, v = g^2
+        opt.step([grad])
+        m, v = eight_bit_values(opt.states[0], n)
+        keep = torch.ones(n, dtype=torch.bool, device=DEV)
+        keep[::128] = False
+        for got, want in ((m[keep], float(grad[1])), (v[keep], float(grad[1]) ** 2)):
+            spread = float(got.std())
+            assert spread > 0
+            assert abs(float(got.mean()) - want) <= 5 * spread / math.sqrt(got.numel()) + 2.0 ** -16 * want
+
+
+def test_8_bit_second_moment_decays():
+    """Without gradients v falls by beta2 each step on average; nearest rounding would keep it."""
+    n = 128 * 64
+    p, g = torch.zeros(n, device=DEV), randn(gen(1), n, 1e-3)
+    opt = T.AdamW([p], lr=0.0, betas=(0.9, 0.999), state_bits=8, weight_decay=0.0)
+    opt.step([g])
+    v0 = eight_bit_values(opt.states[0], n)[1].sum()
+    zero = torch.zeros_like(g)
+    for _ in range(300):
+        opt.step([zero])
+    ratio = float(eight_bit_values(opt.states[0], n)[1].sum() / v0)
+    # the sum of 8192 unbiased terms: a few percent of spread around 0.999^300 = 0.741
+    assert abs(ratio - 0.999 ** 300) < 0.05
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_many_tensors_are_each_alone(bits):
+    """More tensors than one launch's table, lengths from zero to many workgroups: each tensor gets
+    what a call with the others emptied gives it (its place in the list sets the random numbers)."""
+    lengths = [0, 1, 5, 128, 129, 5000, 3, 0, 2048] * 11 + [100000]
+    g = gen(3)
+    params = [randn(g, n, 0.02) for n in lengths]
+    grads = [randn(g, n, 1e-3) for n in lengths]
+    decay = [0.1 * (i % 3) for i in range(len(lengths))]
+    start = [p.clone() for p in params]
+    kw = dict(HYPER, weight_decay=decay, state_bits=bits, seed=9)
+    opt = T.AdamW(params, **kw)
+    opt.step(grads)
+    opt.step(grads)
+    for i in (1, 5, 39, 40, 41, 80, 98, 99):
+        n = lengths[i]
+        alone = [start[j].clone() if j == i else start[j].new_zeros(0) for j in range(len(lengths))]
+        one = T.AdamW(alone, **kw)
+        for _ in range(2):
+            one.step([grads[j] if j == i else grads[j].new_zeros(0) for j in range(len(lengths))])
+        assert torch.equal(alone[i], params[i])
+        for k in one.states[i]:
+            assert torch.equal(one.states[i][k], opt.states[i][k]), (i, k)
+
+
+def test_memory_around_a_tensor_is_left():
+    for bits in (32, 8):
+        n = 1003
+        buf = torch.full((n + 64,), 3.0, device=DEV)
+        st_buf = torch.full((n + 64,), 7, dtype=torch.uint8, device=DEV)
+        p = buf[32:32 + n]
+        opt = T.AdamW([p], state_bits=bits, **HYPER)
+        if bits == 8:
+            st = {"m": st_buf[32:32 + n].zero_(), "v": torch.zeros(n, dtype=torch.uint8, device=DEV),
+                  "m_scales": torch.zeros(8, device=DEV), "v_scales": torch.zeros(8, device=DEV)}
+            opt = T.AdamW([p], state_bits=8, states=[st], **HYPER)
+        opt.step([randn(gen(1), n)])
+        assert (buf[:32] == 3).all() and (buf[32 + n:] == 3).all()
+        assert (st_buf[:32] == 7).all() and (st_buf[32 + n:] == 7).all()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_captured_step_follows_its_device_scalars(bits):
+    """A captured step replayed with advance() between gives the eager steps' bits."""
+    n = 5000
+    g = gen(7)
+    p, grad = randn(g, n, 0.02), randn(g, n, 1e-3)
+    q = p.clone()
+    eager = T.AdamW([p], state_bits=bits, seed=4, **HYPER)
+    taken = T.AdamW([q], state_bits=bits, seed=4, **HYPER)
+    taken.device_scalars
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        taken.step([grad], captured=True)
+    for k in range(4):
+        if k == 2:
+            eager.set_lr(1e-2)
+            taken.set_lr(1e-2)
+        eager.step([grad], grad_scale=0.25 * (k + 1))
+        taken.advance(grad_scale=0.25 * (k + 1))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(p, q)
+        for name in eager.states[0]:
+            assert torch.equal(eager.states[0][name], taken.states[0][name])
+    assert taken.step_count == eager.step_count == 4
+
+
+def test_not_finite_gradients_show():
+    n = 1000
+    for bits in (32, 8):
+        p, g = torch.zeros(n, device=DEV), randn(gen(1), n)
+        g[300] = float("nan")
+        opt = T.AdamW([p], state_bits=bits, **HYPER)
+        opt.step([g])
+        assert p[300].isnan() and int(p.isnan().sum()) == 1
+        if bits == 8:
+            assert opt.states[0]["m_scales"][2].isnan() and opt.states[0]["v_scales"][2].isnan()
+            assert int(opt.states[0]["m_scales"].isnan().sum()) == 1
+
+
+def test_python_refusals():
+    p = torch.zeros(10, device=DEV)
+    for kw in (dict(state_bits=16), dict(copies=[]), dict(copies=[torch.zeros(9, device=DEV)]),
+               dict(states=[{"m": p, "v": torch.zeros(9, device=DEV)}]), dict(weight_decay=[0.1, 0.2]),
+               dict(states=[])):
+        with pytest.raises(ValueError):
+            T.AdamW([p], **kw)
+    with pytest.raises(ValueError):
+        T.AdamW([])
+    with pytest.raises(ValueError):
+        T.AdamW([p, p.half()])
+    opt = T.AdamW([p])
+    for bad in ([], [torch.zeros(9, device=DEV)], [torch.zeros(10)], [torch.zeros(10, device=DEV).double()],
+                [torch.zeros(20, device=DEV)[::2]]):
+        with pytest.raises(ValueError):
+            opt.step(bad)
+    with pytest.raises(B.HQError):
+        T.AdamW([p], betas=(1.0, 0.9)).step([p])
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_training_steps_of_a_block_scaled_layer(bits):
+    """The operators as they are used together: quantize W, forward, both gradients, update, and
+    again from the updated bf16 weights; every stage against the 64-bit one on its own inputs."""
+    N, C, D = 200, 384, 300
+    g = gen(11)
+    master = randn(g, D * C, 0.02)
+    bias = randn(g, D, 0.1)
+    w = master.to(torch.bfloat16).view(D, C)
+    x, dy = randn(g, N * C).view(N, C).bfloat16(), randn(g, N * D, 1e-3).view(N, D).bfloat16()
+    layer = T.BlockLayer(N, C, D)
+    y, dx = torch.empty_like(dy), torch.empty_like(x)
+    dw = torch.zeros(D, C, device=DEV)
+    opt = T.AdamW([master, bias], state_bits=bits, copies=[w.view(-1), torch.zeros(D, dtype=torch.bfloat16, device=DEV)],
+                  **HYPER)
+    for step in range(1, 4):
+        layer.set_weight(w)
+        layer.fwd(x, y)
+        layer.bwd_input(dy, dx)
+        layer.bwd_weight(dw)
+        vw = R.values(w, 128, 128)
+        for got, a, b in ((y, R.values(x, 1, 128), vw), (dx, R.values(dy, 1, 128), vw.t().contiguous()),
+                          (dw, R.values(dy, 128, 1).t().contiguous(), R.values(x, 128, 1).t().contiguous())):
+            want = torch.mm(a, b.t().contiguous())
+            R.assert_within(got, want, R.product_bound(a, b, want, got.dtype), "step %d" % step)
+        grads = [dw.view(-1), dy.float().sum(0)]
+        before = [p.double() for p in (master, bias)]
+        states = [eight_bit_values(s, p.numel()) if bits == 8 else (s["m"].double(), s["v"].double())
+                  for s, p in zip(opt.states, (master, bias))]
+        opt.step(grads)
+        for p, p0, gr, (m, v) in zip((master, bias), before, grads, states):
+            want, _, _, (bp, _, _) = formula(p0, gr.double(), m, v, step)
+            R.assert_within(p, want, stored(want, bp, torch.float32), "p at step %d" % step)
+        assert torch.equal(w.view(-1), master.bfloat16())

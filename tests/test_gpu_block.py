@@ -1,0 +1,400 @@
+"""Block-scaled FP8 operators against 64-bit references: the quantizer (codes and scales equal),
+the products in every form, the layer calls, graphs, streams and refusals."""
+import pytest
+import torch
+
+import train_testlib as R
+from hadamard_rotated_precision_amd import binding as B
+from hadamard_rotated_precision_amd import tensors as T
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+F32, POW2 = B.HQ_BSCALE_F32, B.HQ_BSCALE_POW2
+ROWS, TILES = B.HQ_BLOCK_ROWS, B.HQ_BLOCK_TILES
+
+
+def gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return g
+
+
+def draw(g, rows, cols, dtype=torch.float32, scale=1.0):
+    x = torch.randn(rows, cols, generator=g, device=DEV) * scale
+    if cols > 4:
+        x[:, 3] *= 50
+    return x.to(dtype)
+
+
+def check_quantized(q, x, kind):
+    """Codes and scales of a BlockTensor equal the definition's."""
+    def same(what, got, want):
+        assert torch.equal(got, want), what
+
+    def layout(codes, scales, br, bc, turned):
+        want, s = R.quantize(x, br, bc, kind)
+        same("codes", codes.view(R.E4M3).double(), want.t() if turned else want)
+        return s
+
+    if q.shape == TILES:
+        s = layout(q.codes_view(), q.scales, 128, 128, False) if q.codes is not None else None
+        if q.codes_t is not None:
+            s = layout(q.codes_t_view(), q.scales, 128, 128, True)
+        same("scales", q.scales.double(), s)
+    else:
+        if q.codes is not None:
+            same("scales", q.scales.double(), layout(q.codes_view(), q.scales, 1, 128, False).t())
+        if q.codes_t is not None:
+            same("scales_t", q.scales_t.double(), layout(q.codes_t_view(), q.scales_t, 128, 1, True))
+    for codes, n in ((q.codes, q.cols), (q.codes_t, q.rows)):
+        if codes is not None:   # the pitch's padding is zero
+            assert not codes[:, n:].any()
+
+
+SIZES = [(1, 1), (1, 128), (1, 4096), (3, 17), (16, 129), (127, 127), (128, 128), (129, 130),
+         (257, 1000), (640, 384), (1000, 1030), (2, 20000), (20000, 3)]
+
+
+@pytest.mark.parametrize("rows,cols", SIZES)
+@pytest.mark.parametrize("shape", [ROWS, TILES])
+def test_quantize_sizes(rows, cols, shape):
+    for k, (dtype, kind) in enumerate([(torch.bfloat16, F32), (torch.float16, POW2),
+                                       (torch.float32, F32), (torch.float32, POW2)]):
+        x = draw(gen(rows + cols + k), rows, cols, dtype)
+        check_quantized(T.BlockTensor(rows, cols, shape=shape, scale=kind).quantize(x), x, kind)
+
+
+@pytest.mark.parametrize("shape", [ROWS, TILES])
+def test_quantize_one_layout_alone(shape):
+    x = draw(gen(5), 200, 333, torch.bfloat16)
+    for kw in (dict(codes=False), dict(codes_t=False)):
+        check_quantized(T.BlockTensor(200, 333, shape=shape, **kw).quantize(x), x, F32)
+
+
+@pytest.mark.parametrize("kind", [F32, POW2])
+def test_quantize_extreme_magnitudes(kind):
+    """Blocks of zeros, of one value, of subnormals, near the largest fp32, and spread over the
+    whole exponent range; values on grid points and on midpoints between them."""
+    g = gen(9)
+    x = torch.zeros(256, 512, device=DEV)
+    x[0] = 1.0
+    x[1] = 1e-40
+    x[2] = 3e38 * torch.rand(512, generator=g, device=DEV)
+    x[3] = torch.exp2(torch.rand(512, generator=g, device=DEV) * 250 - 126)
+    x[4, ::2] = 448.0
+    x[5] = 2.0 ** -126
+    points = torch.arange(128, dtype=torch.uint8, device=DEV).view(R.E4M3).float()[:127]
+    x[6, :127], x[6, 127] = points, 448.0
+    x[7, :126], x[7, 127] = (points[1:] + points[:-1]) / 2, 448.0
+    x[8, 5] = -7.0
+    x[128:] = draw(g, 128, 512)
+    check_quantized(T.BlockTensor(256, 512, scale=kind).quantize(x), x, kind)
+    check_quantized(T.BlockTensor(256, 512, shape=TILES, scale=kind).quantize(x), x, kind)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("kind", [F32, POW2])
+def test_not_finite_blocks_are_nan_and_others_are_not(bad, kind):
+    x = draw(gen(2), 200, 300, torch.bfloat16)
+    clean = T.BlockTensor(200, 300, scale=kind).quantize(x)
+    y = x.clone()
+    y[130, 200] = bad
+    q = T.BlockTensor(200, 300, scale=kind).quantize(y)
+    want, want_t = clean.scales.clone(), clean.scales_t.clone()
+    want[1, 130] = want_t[1, 200] = float("nan")
+    assert torch.equal(q.scales.isnan(), want.isnan()) and torch.equal(q.scales_t.isnan(), want_t.isnan())
+    assert torch.equal(q.scales.nan_to_num(0), want.nan_to_num(0))
+    assert not q.codes_view()[130, 128:256].any() and not q.codes_t_view()[200, 128:].any()
+    w = T.BlockTensor(96, 300, shape=TILES, scale=kind).quantize(draw(gen(3), 96, 300))
+    for dtype in (torch.float32, torch.bfloat16):
+        c = torch.zeros(200, 96, dtype=dtype, device=DEV)
+        T.block_gemm(q, w, c)
+        assert c[130].isnan().all() and c.isnan().sum() == 96
+
+
+# M, N, K: one row, tails on every axis, K below, at and above a block
+PRODUCTS = [(1, 1, 1), (1, 16, 128), (1, 777, 1000), (2, 300, 4096), (16, 513, 640), (17, 64, 127),
+            (33, 129, 129), (64, 64, 256), (100, 1000, 272), (256, 256, 512), (300, 260, 1030),
+            (513, 700, 384), (1, 4096, 16), (1000, 3, 200)]
+
+
+def operands(M, N, K, kinds, shapes, seed=0, codes_t=False):
+    g = gen(M + 3 * N + 7 * K + seed)
+    a, b = draw(g, M, K, torch.bfloat16), draw(g, N, K, torch.bfloat16, 0.02)
+    return [T.BlockTensor(*x.shape, shape=s, scale=k, codes_t=codes_t).quantize(x)
+            for x, k, s in ((a, kinds[0], shapes[0]), (b, kinds[1], shapes[1]))]
+
+
+def as_values(q, side=0):
+    """What one layout of a BlockTensor stands for, in fp64."""
+    codes = q.codes_view() if side == 0 else q.codes_t_view()
+    v = codes.view(R.E4M3).double()
+    if q.shape == TILES:
+        s = R.spread(q.scales.double(), 128, 128, (q.rows, q.cols))
+        return v * (s if side == 0 else s.t())
+    s = q.scales if side == 0 else q.scales_t
+    return v * R.spread(s.double().t().contiguous(), 1, 128, v.shape)
+
+
+@pytest.mark.parametrize("M,N,K", PRODUCTS)
+def test_gemm_sizes(M, N, K):
+    for k, (dtype, kinds, shapes) in enumerate([
+            (torch.float32, (F32, F32), (ROWS, TILES)), (torch.bfloat16, (F32, F32), (ROWS, TILES)),
+            (torch.float16, (POW2, POW2), (ROWS, TILES)), (torch.bfloat16, (F32, F32), (ROWS, ROWS)),
+            (torch.bfloat16, (POW2, POW2), (ROWS, ROWS)), (torch.float32, (POW2, F32), (TILES, ROWS)),
+            (torch.float16, (F32, POW2), (TILES, TILES))]):
+        print("[case] gemm", M, N, K, dtype, kinds, shapes, flush=True)
+        a, b = operands(M, N, K, kinds, shapes, k)
+        c = torch.full((M, N), 7.0, dtype=dtype, device=DEV)
+        T.block_gemm(a, b, c)
+        va, vb = as_values(a), as_values(b)
+        want = torch.mm(va, vb.t().contiguous())
+        R.assert_within(c, want, R.product_bound(va, vb, want, dtype), "gemm")
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("M,N,K", [(1, 200, 300), (40, 300, 260), (300, 520, 1000)])
+def test_gemm_accumulates(M, N, K, dtype):
+    a, b = operands(M, N, K, (F32, F32), (ROWS, TILES))
+    c = draw(gen(1), M, N, dtype)
+    va, vb = as_values(a), as_values(b)
+    want = torch.mm(va, vb.t().contiguous()) + c.double()
+    T.block_gemm(a, b, c, accumulate=True)
+    bound = R.product_bound(va, vb, want, dtype) + 2.0 ** -24 * want.abs()
+    R.assert_within(c, want, bound, "accumulate")
+
+
+def test_gemm_leaves_the_memory_around_its_output():
+    for M, N, K in ((5, 77, 200), (130, 131, 140), (257, 300, 300)):
+        a, b = operands(M, N, K, (F32, F32), (ROWS, TILES))
+        for dtype in (torch.float32, torch.bfloat16):
+            buf = torch.full((M * N + 512,), 3.0, dtype=dtype, device=DEV)
+            T.block_gemm(a, b, buf[256:256 + M * N].view(M, N))
+            assert (buf[:256] == 3).all() and (buf[256 + M * N:] == 3).all()
+
+
+def test_gemm_empty_contraction_and_empty_outputs():
+    a, b = T.BlockTensor(5, 0), T.BlockTensor(7, 0, shape=TILES)
+    c = torch.full((5, 7), 2.0, device=DEV)
+    T.block_gemm(a, b, c, accumulate=True)
+    assert (c == 2).all()
+    T.block_gemm(a, b, c)
+    assert (c == 0).all()
+    T.block_gemm(T.BlockTensor(0, 64), T.BlockTensor(7, 64, shape=TILES),
+                 torch.empty(0, 7, device=DEV))
+
+
+def test_exact_products_of_grid_values_and_differences():
+    """Values that the codes hold exactly (E4M3 grid values times a power of two, 448 of it in every
+    block), so the layer is the linear map itself: the forward's differences along one input are
+    the input gradient's terms, along one weight the weight gradient's."""
+    N, C, D = 40, 256, 130
+    g = gen(4)
+
+    def on_grid(rows, cols, scale, axis):
+        x = torch.randint(-8, 9, (rows, cols), generator=g, device=DEV).float()
+        big = torch.zeros_like(x)
+        (big[:, ::128] if axis == 1 else big[::128])[...] = 448.0
+        return torch.where(big > 0, big, x) * scale
+
+    x, w = on_grid(N, C, 0.25, 1), on_grid(D, C, 0.5, 1)
+    dy = on_grid(N, D, 2.0 ** -6, 1)
+    dy[0], x[0] = 448 * 2.0 ** -6, 112.0     # and in every block of tokens
+    layer = T.BlockLayer(N, C, D)
+    y, dx, dw = (torch.empty(s, device=DEV) for s in ((N, D), (N, C), (D, C)))
+    layer.set_weight(w)
+    layer.fwd(x, y)
+    layer.bwd_input(dy, dx)
+    layer.bwd_weight(dw)
+    assert torch.equal(y.double(), x.double() @ w.double().t())
+    assert torch.equal(dx.double(), dy.double() @ w.double())
+    assert torch.equal(dw.double(), dy.double().t() @ x.double())
+    loss = float((y.double() * dy.double()).sum())
+    for n, c in ((3, 5), (17, 130), (39, 255)):
+        x2 = x.clone()
+        x2[n, c] += 0.25
+        y2 = torch.empty_like(y)
+        T.BlockLayer(N, C, D, weight=layer.qw, train=False).fwd(x2, y2)
+        assert float((y2.double() * dy.double()).sum()) - loss == 0.25 * float(dx[n, c])
+    for d, c in ((1, 7), (129, 200)):
+        w2, y2 = w.clone(), torch.empty_like(y)
+        w2[d, c] += 0.5
+        other = T.BlockLayer(N, C, D, train=False)
+        other.set_weight(w2)
+        other.fwd(x, y2)
+        assert float((y2.double() * dy.double()).sum()) - loss == 0.5 * float(dw[d, c])
+
+
+LAYERS = [(1, 128, 128), (1, 1000, 777), (7, 4096, 1024), (16, 640, 4100), (100, 300, 500),
+          (257, 1030, 778), (1000, 512, 640)]
+
+
+@pytest.mark.parametrize("N,C,D", LAYERS)
+@pytest.mark.parametrize("kind", [F32, POW2])
+def test_layer_calls(N, C, D, kind):
+    """Forward, input gradient and weight gradient against products of the definition's codes; the
+    saved tensors; the serving form gives the forward's bits."""
+    for dtype in (torch.bfloat16, torch.float32):
+        print("[case] layer", N, C, D, kind, dtype, flush=True)
+        g = gen(N + C + D)
+        x, w, dy = draw(g, N, C, dtype), draw(g, D, C, dtype, 0.02), draw(g, N, D, dtype, 1e-3)
+        layer = T.BlockLayer(N, C, D, scale=kind)
+        y, dx = torch.empty(N, D, dtype=dtype, device=DEV), torch.empty(N, C, dtype=dtype, device=DEV)
+        dw = torch.empty(D, C, dtype=dtype, device=DEV)
+        layer.set_weight(w)
+        layer.fwd(x, y)
+        layer.bwd_input(dy, dx)
+        layer.bwd_weight(dw)
+        for q, t in ((layer.qx, x), (layer.qg, dy)):
+            check_quantized(q, t, kind)
+        check_quantized(layer.qw, w, kind)
+        vw = R.values(w, 128, 128, kind)
+        for what, got, a, b in (
+                ("y", y, R.values(x, 1, 128, kind), vw),
+                ("dx", dx, R.values(dy, 1, 128, kind), vw.t().contiguous()),
+                ("dw", dw, R.values(dy, 128, 1, kind).t().contiguous(),
+                 R.values(x, 128, 1, kind).t().contiguous())):
+            want = torch.mm(a, b.t().contiguous())
+            R.assert_within(got, want, R.product_bound(a, b, want, dtype), what)
+        y2 = torch.full_like(y, 5.0)
+        T.BlockLayer(N, C, D, scale=kind, weight=layer.qw, train=False).fwd(x, y2)
+        assert torch.equal(y, y2)
+        dw2 = dw.clone()
+        layer.bwd_weight(dw2, accumulate=True)
+        assert torch.allclose(dw2.float(), 2 * dw.float(), rtol=2.0 ** -6, atol=1e-9)
+
+
+def test_wrapped_weights_with_wide_pitches():
+    """Codes and scales that exist already, in pitches wider than needed; junk behind the padding
+    changes nothing."""
+    N, C, D = 9, 300, 200
+    x, w = draw(gen(1), N, C, torch.bfloat16), draw(gen(2), D, C, torch.bfloat16, 0.02)
+    q = T.BlockTensor(D, C, shape=TILES).quantize(w)
+    codes = torch.full((D, 400), 0x7E, dtype=torch.uint8, device=DEV)
+    codes[:, :304] = q.codes
+    scales = torch.full((2, 8), float("nan"), device=DEV)
+    scales[:, :3] = q.scales
+    wrapped = T.BlockTensor.wrap(codes, scales, D, C)
+    for n in (N, 1, 200):
+        xs = draw(gen(3), n, C, torch.bfloat16)
+        y, y2 = (torch.empty(n, D, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+        T.BlockLayer(n, C, D, weight=q, train=False).fwd(xs, y)
+        T.BlockLayer(n, C, D, weight=wrapped, train=False).fwd(xs, y2)
+        assert torch.equal(y, y2)
+    with pytest.raises(ValueError):
+        T.BlockTensor.wrap(codes, scales[:, :2], D, C)
+    with pytest.raises(ValueError):
+        T.BlockTensor.wrap(codes, q.scales, D, C, scale=POW2)
+
+
+def test_python_refusals():
+    layer = T.BlockLayer(8, 64, 32)
+    x, y = torch.zeros(8, 64, device=DEV), torch.zeros(8, 32, device=DEV)
+    for bad in (x[:4], x.double(), torch.zeros(64, 8, device=DEV).t(), x.cpu()):
+        with pytest.raises(ValueError):
+            layer.fwd(bad, y)
+    with pytest.raises(ValueError):
+        T.BlockLayer(8, 64, 32, train=False).bwd_weight(torch.zeros(32, 64, device=DEV))
+    with pytest.raises(ValueError):
+        T.BlockLayer(8, 64, 32, weight=T.BlockTensor(32, 48, shape=TILES))
+    with pytest.raises(B.HQError):   # weights without a transposed layout
+        T.BlockLayer(8, 64, 32, weight=T.BlockTensor(32, 64, shape=TILES, codes_t=False)).bwd_input(y, x)
+
+
+STEPS = [(3, 500, 300), (300, 512, 640), (1000, 1030, 778)]
+
+
+class Step:
+    def __init__(self, N, C, D, dtype, kind, seed):
+        g = gen(seed)
+        self.x, self.w = draw(g, N, C, dtype), draw(g, D, C, dtype, 0.02)
+        self.dy = draw(g, N, D, dtype, 1e-3)
+        self.layer = T.BlockLayer(N, C, D, scale=kind)
+        self.y, self.dx = torch.empty_like(self.dy), torch.empty_like(self.x)
+        self.dw = torch.empty_like(self.w)
+
+    def run(self, stream=None):
+        self.layer.set_weight(self.w, stream)
+        self.layer.fwd(self.x, self.y, stream)
+        self.layer.bwd_input(self.dy, self.dx, stream)
+        self.layer.bwd_weight(self.dw, stream=stream)
+
+    def outputs(self):
+        q = [t for b in (self.layer.qx, self.layer.qw, self.layer.qg)
+             for t in (b.codes, b.codes_t, b.scales, b.scales_t) if t is not None]
+        return [t.clone() for t in [self.y, self.dx, self.dw] + q]
+
+    def scramble(self):
+        for t in (self.y, self.dx, self.dw):
+            t.fill_(3.0)
+        self.layer.ws.fill_(0xAB)
+
+
+@pytest.mark.parametrize("N,C,D", STEPS)
+def test_captured_steps_replay_to_the_eager_bits(N, C, D):
+    """Two captured graphs with workspaces of their own, replayed in turn with eager work between."""
+    for dtype, kind in ((torch.bfloat16, F32), (torch.float32, POW2)):
+        a, b = Step(N, C, D, dtype, kind, 1), Step(N, C, D, dtype, kind, 2)
+        want = []
+        for s in (a, b):
+            s.run()
+            torch.cuda.synchronize()
+            want.append(s.outputs())
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            a.run()
+            b.run()
+        torch.cuda.current_stream().wait_stream(side)
+        graphs = []
+        for s in (a, b):
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                s.run()
+            graphs.append(graph)
+        for rep in range(3):
+            for s in (a, b):
+                s.scramble()
+            torch.cuda.synchronize()
+            for graph in graphs:
+                graph.replay()
+            torch.cuda.synchronize()
+            for s, w in zip((a, b), want):
+                for i, (got, ref) in enumerate(zip(s.outputs(), w)):
+                    assert torch.equal(got, ref), (rep, i)
+                s.run()
+        torch.cuda.synchronize()
+
+
+def test_two_streams_give_what_each_gives_alone():
+    a, b = Step(600, 1030, 778, torch.bfloat16, F32, 1), Step(5, 2048, 1500, torch.bfloat16, POW2, 2)
+    want = []
+    for s in (a, b):
+        s.run()
+        torch.cuda.synchronize()
+        want.append(s.outputs())
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for rep in range(3):
+        for s in (a, b):
+            s.scramble()
+        torch.cuda.synchronize()
+        for _ in range(4):
+            a.run(s1)
+            b.run(s2)
+        torch.cuda.synchronize()
+        for s, w in zip((a, b), want):
+            for got, ref in zip(s.outputs(), w):
+                assert torch.equal(got, ref)
+
+
+def test_one_row_of_a_batch_does_not_depend_on_the_others():
+    """A padded batch: rows of zeros, and other rows' values, leave a row's output alone."""
+    C, D = 700, 390
+    w = T.BlockTensor(D, C, shape=TILES).quantize(draw(gen(1), D, C, torch.bfloat16, 0.02))
+    x = draw(gen(2), 40, C, torch.bfloat16)
+    y = torch.empty(40, D, dtype=torch.bfloat16, device=DEV)
+    T.BlockLayer(40, C, D, weight=w, train=False).fwd(x, y)
+    x2, y2 = x.clone(), torch.empty_like(y)
+    x2[20:] = 0
+    T.BlockLayer(40, C, D, weight=w, train=False).fwd(x2, y2)
+    assert torch.equal(y[:20], y2[:20]) and not y2[20:].any()
