@@ -11,6 +11,7 @@
 // neighbouring lanes.
 #include "hq_device.hpp"
 #include "hq_launch.hpp"
+#include "hq_train_device.hpp"
 #include "hq_train_internal.hpp"
 
 namespace hq {
@@ -48,62 +49,6 @@ __device__ inline uint32_t mix32(uint32_t h) {
   h ^= h >> 15;
   h *= 2891336453u;
   return h ^ (h >> 16);
-}
-
-// Eight elements from element i on, n of them valid (the rest 0).
-template <class T>
-__device__ inline void get8(const void* base, int64_t i, int n, float (&v)[8]) {
-  if (n >= 8) {
-    const char* p = static_cast<const char*>(base) + i * T::bytes;
-    if constexpr (T::bytes == 4) {
-      const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else {
-      const uint4 q = *reinterpret_cast<const uint4*>(p);
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[2 * j] = T::from_bits(static_cast<uint16_t>(w[j] & 0xFFFFu));
-        v[2 * j + 1] = T::from_bits(static_cast<uint16_t>(w[j] >> 16));
-      }
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = j < n ? T::load(base, i + j) : 0.0f;
-  }
-}
-
-// A bf16 rounding that keeps NaN (the shared one takes finite values).
-template <class T>
-__device__ inline void put1(void* base, int64_t i, float v) {
-  if constexpr (T::is_bf16) {
-    static_cast<uint16_t*>(base)[i] = static_cast<uint16_t>(T::pack2(v, 0.0f));
-  } else {
-    T::store(base, i, v);
-  }
-}
-
-template <class T>
-__device__ inline void put8(void* base, int64_t i, int n, const float (&v)[8]) {
-  if (n >= 8) {
-    char* p = static_cast<char*>(base) + i * T::bytes;
-    if constexpr (T::bytes == 4) {
-      reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-      reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-      uint4 q;
-      q.x = T::pack2(v[0], v[1]);
-      q.y = T::pack2(v[2], v[3]);
-      q.z = T::pack2(v[4], v[5]);
-      q.w = T::pack2(v[6], v[7]);
-      *reinterpret_cast<uint4*>(p) = q;
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < n) put1<T>(base, i + j, v[j]);
-  }
 }
 
 // Eight code bytes from element i on (bytes past n read as 0 and are not written).
@@ -196,8 +141,8 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs g) {
   if (!EIGHT && n == 0) return;
 
   float p[8], gr[8], m[8], v[8];
-  get8<P>(t.p, i, n, p);
-  get8<G>(t.grad, i, n, gr);
+  load8<P>(t.p, i, n, true, p);
+  load8<G>(t.grad, i, n, true, gr);
   if constexpr (EIGHT) {
     const float ms = n > 0 ? t.ms[i >> 7] : 0.0f, vs = n > 0 ? t.vs[i >> 7] : 0.0f;
     e4m3_values(get_codes(t.m, i, n), m);
@@ -209,8 +154,8 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs g) {
       v[j] *= v[j];
     }
   } else {
-    get8<F32>(t.m, i, n, m);
-    get8<F32>(t.v, i, n, v);
+    load8<F32>(t.m, i, n, true, m);
+    load8<F32>(t.v, i, n, true, v);
   }
   const float keep = 1.0f - s.lr * t.wd;
 #pragma unroll
@@ -221,11 +166,11 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs g) {
     const float den = sqrtf(v[j]) * s.inv_sqrt_bias2 + g.eps;
     p[j] = p[j] * keep - s.step_size * m[j] / den;
   }
-  put8<P>(t.p, i, n, p);
-  if (t.copy) put8<C>(t.copy, i, n, p);
+  store8<P>(t.p, i, n, true, p);
+  if (t.copy) store8<C>(t.copy, i, n, true, p);
   if constexpr (!EIGHT) {
-    put8<F32>(t.m, i, n, m);
-    put8<F32>(t.v, i, n, v);
+    store8<F32>(t.m, i, n, true, m);
+    store8<F32>(t.v, i, n, true, v);
   } else {
     float y[8];
 #pragma unroll

@@ -17,6 +17,7 @@
 // LDS and leave as 16-byte pieces of the transposed rows.
 #include "hq_device.hpp"
 #include "hq_launch.hpp"
+#include "hq_train_device.hpp"
 #include "hq_train_internal.hpp"
 
 namespace hq {
@@ -46,30 +47,6 @@ __device__ inline void block_scale(uint32_t a, bool pow2, float& s, float& r) {
   r = 1.0f / s;
   if (a == 0u) s = 0.0f, r = 0.0f;
   if (a >= 0x7F800000u) s = __uint_as_float(0x7FC00000u), r = 0.0f;
-}
-
-// Eight elements from element i of the source (n of them valid).
-template <class T>
-__device__ inline void load8(const void* src, int64_t i, int n, bool vec, float (&v)[8]) {
-  if (vec && n >= 8) {
-    const char* p = static_cast<const char*>(src) + i * T::bytes;
-    if constexpr (T::bytes == 4) {
-      const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else {
-      const uint4 q = *reinterpret_cast<const uint4*>(p);
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[2 * j] = T::from_bits(static_cast<uint16_t>(w[j] & 0xFFFFu));
-        v[2 * j + 1] = T::from_bits(static_cast<uint16_t>(w[j] >> 16));
-      }
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = j < n ? T::load(src, i + j) : 0.0f;
-  }
 }
 
 __device__ inline uint32_t mag(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }

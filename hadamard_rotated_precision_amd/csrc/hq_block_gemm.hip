@@ -1,20 +1,29 @@
 // hq_block_gemm.hip — product of block-scaled FP8 matrices on the matrix cores:
 //   c[m][n] (+)= sum_kb sa(m,kb) sb(n,kb) sum_{k in kb} a[m][k] b[n][k],  kb = blocks of 128.
 //
-// Per block the codes are multiplied into fresh accumulators, and acc += t (sa sb) follows in fp32.
+// In the kernels P is the operand along the accumulator's registers (b: output columns, four
+// consecutive ones per lane) and Q the one along the lanes (a: output rows).
+#include <type_traits>
+
 #include "hq_device.hpp"
 #include "hq_launch.hpp"
+#include "hq_train_device.hpp"
 #include "hq_train_internal.hpp"
 
 namespace hq {
 
+typedef float v4f __attribute__((ext_vector_type(4)));
 typedef float v16f __attribute__((ext_vector_type(16)));
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef int v8i __attribute__((ext_vector_type(8)));
 typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 
+constexpr int kFar = 0x7FFFFFF0;   // an offset past any descriptor: the load reads 0
+
 struct BlockGemmArgs {
-  BlockOperand a, b;
-  int64_t M, N, K;
+  BlockOperand p, q;       // b and a
+  int64_t M, N, K;         // q rows, p rows, contraction
   void* c;
   int accumulate;
 };
@@ -28,16 +37,249 @@ __device__ inline v8h f8_to_h8(uint2 q) {
   return v8h{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// One wave per 32 x 32 tile, fragments straight from memory: v_mfma_f32_32x32x16_f16 with b's rows
-// along the accumulator's registers (row 8 (r/4) + 4 (lane/32) + r%4) and a's rows along the lanes.
+// ------------------------------------------------------------------ tiled kernel (FP8 instruction)
+// How the scales come in:
+//   S_TILES: p's scale is one number per wave and K step (a wave's P rows lie inside one 128-row
+//            block), q's one per lane: f = sp sq, then acc = t f + acc, one fma per value;
+//   S_ROWS:  p has a scale for each row: acc = t (sp sq) + acc, a multiplication and an fma;
+//   S_POW2:  both are powers of two: the instruction takes their exponents and adds to acc itself.
+enum ScaleMode { S_TILES = 0, S_ROWS = 1, S_POW2 = 2 };
+
+// LDS rows of 128 bytes (one block of K); the 16-byte chunk index is XORed with (row / 2) % 8, so
+// the 128-bit reads of 16 consecutive rows at one chunk meet 16 different bank groups.
+__device__ inline int lds_at(int row, int chunk) { return row * 128 + ((chunk ^ ((row >> 1) & 7)) << 4); }
+
+__device__ inline v8i join(v4i a, v4i b) { return v8i{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}; }
+
+// One dword per lane straight into LDS (lane l at lds + 4 l).
+__device__ inline void lds_dma4(__amdgpu_buffer_rsrc_t rs, float* lds, int voffset) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)lds, 4, voffset, 0, 0, 0);
+}
+
+template <class Out, int MODE, int NWP, int NWQ, int TP, int TQ>
+__global__ __launch_bounds__(64 * NWP * NWQ, 1) void block_gemm_kernel(BlockGemmArgs g) {
+  constexpr int NW = NWP * NWQ;
+  constexpr int BP = NWP * TP * 16, BQ = NWQ * TQ * 16;    // workgroup tile
+  constexpr int P_BYTES = BP * 128, Q_BYTES = BQ * 128;
+  constexpr int STAGE = P_BYTES + Q_BYTES + (BP + BQ) * 4;
+  constexpr int PL = BP / 8 / NW, QL = BQ / 8 / NW;        // 1 KB direct-to-LDS loads per wave
+  constexpr int SL = (BP + BQ) / 64;                       // 64-row scale loads of the workgroup
+  static_assert(BP % (8 * NW) == 0 && BQ % (8 * NW) == 0 && SL == NW && BP % 64 == 0 && BQ % 64 == 0, "");
+  __shared__ __attribute__((aligned(16))) int8_t st0[STAGE];
+  __shared__ __attribute__((aligned(16))) int8_t st1[STAGE];
+
+  // XCD-contiguous order: workgroup b runs on XCD b % 8; each XCD gets consecutive tiles, in
+  // groups of 8 q tiles that share p rows in its L2
+  const int tiles_q = static_cast<int>((g.M + BQ - 1) / BQ), tiles_p = static_cast<int>((g.N + BP - 1) / BP);
+  const int ntiles = tiles_q * tiles_p;
+  const int xcd = blockIdx.x & 7, q8 = ntiles >> 3, r8 = ntiles & 7;
+  const int pid = xcd * q8 + min(xcd, r8) + (blockIdx.x >> 3);
+  constexpr int kGroup = 8;
+  const int group = pid / (kGroup * tiles_p), first = group * kGroup;
+  const int gsize = min(tiles_q - first, kGroup);
+  const int tq = first + (pid % (kGroup * tiles_p)) % gsize;
+  const int tp = (pid % (kGroup * tiles_p)) / gsize;
+  const int64_t p0 = static_cast<int64_t>(tp) * BP, q0 = static_cast<int64_t>(tq) * BQ;
+
+  const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int wp = w / NWQ, wq = w % NWQ, lr = lane & 15, lg = lane >> 4;
+
+  // operand descriptors from the tile's first row: rows past the end read as zero
+  const int rows_p = static_cast<int>(min<int64_t>(BP, g.N - p0)), rows_q = static_cast<int>(min<int64_t>(BQ, g.M - q0));
+  const int ldp = static_cast<int>(g.p.ld), ldq = static_cast<int>(g.q.ld);
+  const __amdgpu_buffer_rsrc_t rsp = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint8_t*>(g.p.codes + p0 * g.p.ld), 0, rows_p * ldp, kBufferFlags);
+  const __amdgpu_buffer_rsrc_t rsq = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint8_t*>(g.q.codes + q0 * g.q.ld), 0, rows_q * ldq, kBufferFlags);
+  // lane's place in a 1 KB load: 8 rows of 128 bytes; it fetches the chunk its swizzled slot holds
+  // (the same for every load: rows advance by multiples of 16)
+  const int dr = 8 * w + (lane >> 3), dc = ((lane & 7) ^ ((dr >> 1) & 7)) << 4;
+  const int vp = dr * ldp + dc, vq = dr * ldq + dc;
+  const int K16 = static_cast<int>((g.K + 15) & ~int64_t{15});
+  const int KT = static_cast<int>((g.K + 127) / 128);
+
+  // scales: each wave fetches those of 64 rows (q's first) for each K step
+  const bool s_is_q = w < BQ / 64;
+  const BlockOperand& so = s_is_q ? g.q : g.p;
+  const int64_t s_row0 = s_is_q ? q0 + 64 * w : p0 + 64 * (w - BQ / 64);
+  const int64_t s_rows = s_is_q ? g.M : g.N;
+  const int64_t s_first = so.tiles ? s_row0 >> 7 : s_row0;                      // group of the first row
+  const int64_t s_last = so.tiles ? (s_rows - 1) >> 7 : s_rows - 1;             // of the last valid row
+  const int s_voff = so.tiles ? 0 : lane * 4;
+  const bool s_in = (so.tiles ? s_row0 + lane < s_rows : s_first + lane <= s_last);
+  const float* s_base = so.scales + s_first * so.sg;
+
+  auto dma = [&](int kt, int8_t* stg) {
+    const int k0 = kt * 128;
+    const bool in = kt < KT && k0 + dc < K16;
+    const unsigned bp = in ? vp + k0 : kFar, bq = in ? vq + k0 : kFar;
+#pragma unroll
+    for (int i = 0; i < QL; ++i) lds_dma16(rsq, stg + P_BYTES + (w + NW * i) * 1024, bq + i * NW * 8 * ldq);
+#pragma unroll
+    for (int i = 0; i < PL; ++i) lds_dma16(rsp, stg + (w + NW * i) * 1024, bp + i * NW * 8 * ldp);
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<float*>(s_base + static_cast<int64_t>(min(kt, KT - 1)) * so.sk), 0, 256, kBufferFlags);
+    lds_dma4(rs, reinterpret_cast<float*>(stg + P_BYTES + Q_BYTES) + 64 * w, s_in ? s_voff : kFar);
+  };
+  // fragments of v_mfma_f32_16x16x128_f8f6f4: lane group lg holds 32 of the 128 K bytes of row lr;
+  // chunks lg and lg + 4, the same for both operands, so products pair equal K whatever the
+  // instruction's own order of bytes
+  auto frag = [&](const int8_t* base, int row) {
+    return join(*reinterpret_cast<const v4i*>(base + lds_at(row, lg)),
+                *reinterpret_cast<const v4i*>(base + lds_at(row, lg + 4)));
+  };
+  auto p_frag = [&](const int8_t* stg, int i) { return frag(stg, wp * TP * 16 + i * 16 + lr); };
+  auto q_frag = [&](const int8_t* stg, int j) { return frag(stg + P_BYTES, wq * TQ * 16 + j * 16 + lr); };
+  auto q_scale = [&](const int8_t* stg, int j) {
+    return reinterpret_cast<const float*>(stg + P_BYTES + Q_BYTES)[wq * TQ * 16 + j * 16 + lr];
+  };
+  auto p_scales = [&](const int8_t* stg) { return reinterpret_cast<const float*>(stg + P_BYTES + Q_BYTES) + BQ + wp * TP * 16; };
+
+  v4f acc[TP][TQ];
+#pragma unroll
+  for (int i = 0; i < TP; ++i)
+#pragma unroll
+    for (int j = 0; j < TQ; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  v8i qf[TQ], pf[2];
+  float f[TQ];          // S_TILES: sp sq; S_ROWS: sq
+  int qe[TQ];           // S_POW2: exponent bytes
+
+  auto load_scales = [&](const int8_t* stg) {
+#pragma unroll
+    for (int j = 0; j < TQ; ++j) {
+      const float s = q_scale(stg, j);
+      if constexpr (MODE == S_TILES) f[j] = s * p_scales(stg)[0];
+      else if constexpr (MODE == S_ROWS) f[j] = s;
+      else qe[j] = __float_as_int(s) >> 23;
+    }
+  };
+  // row i of tiles against every q tile
+  auto row = [&](const int8_t* stg, int i, const v8i& p) {
+    if constexpr (MODE == S_POW2) {
+      const int pe = __float_as_int(p_scales(stg)[i * 16 + lr]) >> 23;
+#pragma unroll
+      for (int j = 0; j < TQ; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(p, qf[j], acc[i][j], 0, 0, 0, pe, 0, qe[j]);
+    } else {
+      v4f sp;
+      if constexpr (MODE == S_ROWS) sp = *reinterpret_cast<const v4f*>(p_scales(stg) + i * 16 + 4 * lg);
+#pragma unroll
+      for (int j = 0; j < TQ; ++j) {
+        const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
+        const v4f u = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(p, qf[j], zero, 0, 0, 0, 0, 0, 0);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          if constexpr (MODE == S_TILES) acc[i][j][r] = __builtin_fmaf(u[r], f[j], acc[i][j][r]);
+          else acc[i][j][r] = __builtin_fmaf(u[r], sp[r] * f[j], acc[i][j][r]);
+        }
+      }
+    }
+  };
+  // One barrier per K step. Step kt: rows of tiles 0 .. TP-2 with the next row's fragment read
+  // ahead; then this wave's loads of stage kt+1 have landed and its reads of stage kt are done, and
+  // after the barrier everybody's: stage kt's buffer takes the loads of step kt+2 while the last
+  // row of tiles runs and the first fragments of stage kt+1 are read.
+  auto step = [&](int kt, int8_t* cur, int8_t* nxt) {
+#pragma unroll
+    for (int i = 0; i + 1 < TP; ++i) {
+      pf[(i + 1) & 1] = p_frag(cur, i + 1);
+      row(cur, i, pf[i & 1]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    // the last row's scales come from stage kt too
+    v4f sp_last = {0.0f, 0.0f, 0.0f, 0.0f};
+    int pe_last = 0;
+    if constexpr (MODE == S_ROWS) sp_last = *reinterpret_cast<const v4f*>(p_scales(cur) + (TP - 1) * 16 + 4 * lg);
+    if constexpr (MODE == S_POW2) pe_last = __float_as_int(p_scales(cur)[(TP - 1) * 16 + lr]) >> 23;
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    dma(kt + 2, cur);
+    const v8i p = pf[(TP - 1) & 1];
+#pragma unroll
+    for (int j = 0; j < TQ; ++j) {
+      if constexpr (MODE == S_POW2) {
+        acc[TP - 1][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(p, qf[j], acc[TP - 1][j], 0, 0, 0, pe_last, 0, qe[j]);
+      } else {
+        const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
+        const v4f u = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(p, qf[j], zero, 0, 0, 0, 0, 0, 0);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          if constexpr (MODE == S_TILES) acc[TP - 1][j][r] = __builtin_fmaf(u[r], f[j], acc[TP - 1][j][r]);
+          else acc[TP - 1][j][r] = __builtin_fmaf(u[r], sp_last[r] * f[j], acc[TP - 1][j][r]);
+        }
+      }
+      qf[j] = q_frag(nxt, j);
+    }
+    pf[0] = p_frag(nxt, 0);
+    load_scales(nxt);
+  };
+  static_assert(TP % 2 == 0, "row 0's fragment is in pf[0]");
+
+  if (KT > 0) {
+    dma(0, st0);
+    dma(1, st1);
+    // the loads of stage 0 have landed: those of stage 1 stay in flight
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(PL + QL + 1) : "memory");
+    __builtin_amdgcn_s_barrier();
+#pragma unroll
+    for (int j = 0; j < TQ; ++j) qf[j] = q_frag(st0, j);
+    pf[0] = p_frag(st0, 0);
+    load_scales(st0);
+    int kt = 0;
+    for (; kt + 1 < KT; kt += 2) {
+      step(kt, st0, st1);
+      step(kt + 1, st1, st0);
+    }
+    if (kt < KT) step(kt, st0, st1);
+  }
+  // loads past K (zeros) have landed before the stages are used again
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  __syncthreads();
+
+  // Epilogue, a wave alone: a strip of 16 output rows goes through the wave's part of a stage, so
+  // that lanes hold eight consecutive outputs of a row and neighbouring lanes continue it.
+  constexpr int W = TP * 16, PITCH = W + 4;
+  static_assert(16 * PITCH * 4 * ((NW + 1) / 2) <= STAGE, "the strips of half the waves must fit a stage");
+  float* const strip = reinterpret_cast<float*>((w & 1) ? st1 : st0) + (w >> 1) * 16 * PITCH;
+  constexpr int LPR = W / 8, RPI = 64 / LPR;     // lanes per output row, rows per pass
+#pragma unroll
+  for (int j = 0; j < TQ; ++j) {
+#pragma unroll
+    for (int i = 0; i < TP; ++i) *reinterpret_cast<v4f*>(strip + lr * PITCH + i * 16 + 4 * lg) = acc[i][j];
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+    for (int h = 0; h < 16 / RPI; ++h) {
+      const int sr = h * RPI + lane / LPR, sc = 8 * (lane % LPR);
+      const v4f a = *reinterpret_cast<const v4f*>(strip + sr * PITCH + sc);
+      const v4f b = *reinterpret_cast<const v4f*>(strip + sr * PITCH + sc + 4);
+      float u[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+      const int64_t m = q0 + wq * TQ * 16 + j * 16 + sr, n = p0 + wp * W + sc;
+      if (m < g.M && n < g.N) {
+        const int64_t off = m * g.N + n;
+        if (g.accumulate) {
+          float old[8];
+          load_run<Out>(g.c, off, g.N - n, old);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) u[e] += old[e];
+        }
+        put_run<Out>(g.c, off, g.N - n, u);
+      }
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  }
+}
+
+// ------------------------------------------------------------------ plain kernel (fp16 instruction)
+// One wave per 32 x 32 tile, fragments straight from memory: v_mfma_f32_32x32x16_f16 on the codes
+// as fp16 values, whose sums are as exact as fp32 ones (the FP8 instruction's sum keeps 17 bits).
 template <class Out>
 __global__ __launch_bounds__(64) void block_gemm_plain_kernel(BlockGemmArgs g) {
   const int lane = threadIdx.x, half = lane >> 5;
   const int64_t tiles_n = (g.N + 31) / 32;
   const int64_t m = blockIdx.x / tiles_n * 32 + (lane & 31), n0 = blockIdx.x % tiles_n * 32;
   const int64_t n = n0 + (lane & 31);
-  const uint8_t* pa = g.a.codes + m * g.a.ld;
-  const uint8_t* pb = g.b.codes + n * g.b.ld;
+  const uint8_t* pa = g.q.codes + m * g.q.ld;
+  const uint8_t* pb = g.p.codes + n * g.p.ld;
   v16f acc = {};
   const int64_t K16 = (g.K + 15) / 16 * 16;
   for (int64_t kb = 0; kb * 128 < g.K; ++kb) {
@@ -49,11 +291,11 @@ __global__ __launch_bounds__(64) void block_gemm_plain_kernel(BlockGemmArgs g) {
       if (k < K16 && n < g.N) qb = *reinterpret_cast<const uint2*>(pb + k);
       t = __builtin_amdgcn_mfma_f32_32x32x16_f16(f8_to_h8(qb), f8_to_h8(qa), t, 0, 0, 0);
     }
-    const float sa = m < g.M ? g.a.scales[(g.a.tiles ? m / 128 : m) * g.a.sg + kb * g.a.sk] : 0.0f;
+    const float sa = m < g.M ? g.q.scales[(g.q.tiles ? m / 128 : m) * g.q.sg + kb * g.q.sk] : 0.0f;
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
       const int64_t nr = n0 + 8 * (r >> 2) + 4 * half + (r & 3);
-      const float sb = nr < g.N ? g.b.scales[(g.b.tiles ? nr / 128 : nr) * g.b.sg + kb * g.b.sk] : 0.0f;
+      const float sb = nr < g.N ? g.p.scales[(g.p.tiles ? nr / 128 : nr) * g.p.sg + kb * g.p.sk] : 0.0f;
       acc[r] = __builtin_fmaf(t[r], sa * sb, acc[r]);
     }
   }
@@ -63,21 +305,39 @@ __global__ __launch_bounds__(64) void block_gemm_plain_kernel(BlockGemmArgs g) {
     const int64_t nr = n0 + 8 * (r >> 2) + 4 * half + (r & 3);
     if (nr < g.N) {
       const float old = g.accumulate ? Out::load(g.c, m * g.N + nr) : 0.0f;
-      Out::store(g.c, m * g.N + nr, acc[r] + old);
+      put_one<Out>(g.c, m * g.N + nr, acc[r] + old);
     }
   }
 }
 
 size_t block_gemm_ws(int64_t, int64_t, int64_t) { return 0; }
 
+template <class Out, int MODE, int NWP, int NWQ, int TP, int TQ>
+static hipError_t launch_tiled(const BlockGemmArgs& a, hipStream_t st, int tok) {
+  constexpr int BP = NWP * TP * 16, BQ = NWQ * TQ * 16;
+  const int64_t tiles = ((a.M + BQ - 1) / BQ) * ((a.N + BP - 1) / BP);
+  return launch_k(block_gemm_kernel<Out, MODE, NWP, NWQ, TP, TQ>, dim3(static_cast<unsigned>(tiles)),
+                  dim3(64 * NWP * NWQ), st, tok, a);
+}
+
+template <class Out>
+static hipError_t launch_16bit(const BlockGemmPass& p, const BlockGemmArgs& a, hipStream_t st, int tok) {
+  const int mode = (p.a.pow2 && p.b.pow2) ? S_POW2 : (p.b.tiles ? S_TILES : S_ROWS);
+  switch (mode) {
+    case S_TILES: return launch_tiled<Out, S_TILES, 2, 4, 8, 4>(a, st, tok);
+    case S_ROWS: return launch_tiled<Out, S_ROWS, 2, 4, 8, 4>(a, st, tok);
+    default: return launch_tiled<Out, S_POW2, 2, 4, 8, 4>(a, st, tok);
+  }
+}
+
 hipError_t block_gemm_pass(const BlockGemmPass& p, hipStream_t st) {
-  BlockGemmArgs a{p.a, p.b, p.M, p.N, p.K, p.c, p.accumulate};
+  BlockGemmArgs a{p.b, p.a, p.M, p.N, p.K, p.c, p.accumulate};
   const int tok = prof_open(K_GEMM, 2.0 * p.M * p.N * p.K);
   const dim3 grid(static_cast<unsigned>(((p.M + 31) / 32) * ((p.N + 31) / 32)));
   switch (p.out_dt) {
     case DT_F32: return launch_k(block_gemm_plain_kernel<F32>, grid, dim3(64), st, tok, a);
-    case DT_F16: return launch_k(block_gemm_plain_kernel<F16>, grid, dim3(64), st, tok, a);
-    case DT_BF16: return launch_k(block_gemm_plain_kernel<BF16>, grid, dim3(64), st, tok, a);
+    case DT_F16: return launch_16bit<F16>(p, a, st, tok);
+    case DT_BF16: return launch_16bit<BF16>(p, a, st, tok);
   }
   return hipErrorInvalidValue;
 }

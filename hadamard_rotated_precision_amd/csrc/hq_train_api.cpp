@@ -64,11 +64,11 @@ hq_status check_out(const hq_block_tensor* q, int64_t rows, int64_t cols, int32_
   if (!tiles && q->codes_t && !q->scales_t) return HQ_ERR_NULL;
   if (q->codes) {
     if (!aligned(q->codes, 16) || q->ld % 16) return HQ_ERR_ALIGN;
-    if (q->ld < cols || q->ld > 2 * kMaxDim) return HQ_ERR_SHAPE;
+    if (q->ld < cols || q->ld >= 2 * kMaxDim) return HQ_ERR_SHAPE;
   }
   if (q->codes_t) {
     if (!aligned(q->codes_t, 16) || q->ld_t % 16) return HQ_ERR_ALIGN;
-    if (q->ld_t < rows || q->ld_t > 2 * kMaxDim) return HQ_ERR_SHAPE;
+    if (q->ld_t < rows || q->ld_t >= 2 * kMaxDim) return HQ_ERR_SHAPE;
   }
   if (q->scales && !aligned(q->scales, 4)) return HQ_ERR_ALIGN;
   if (q->scales_t && !aligned(q->scales_t, 4)) return HQ_ERR_ALIGN;
@@ -92,7 +92,7 @@ hq_status check_operand(const hq_block_tensor* q, int32_t side, int64_t rows, in
   if (!codes || !scales) return HQ_ERR_NULL;
   const int64_t ld = t ? q->ld_t : q->ld, len = t ? q->rows : q->cols;
   if (!aligned(codes, 16) || ld % 16 || !aligned(scales, 4)) return HQ_ERR_ALIGN;
-  if (ld < len || ld > 2 * kMaxDim) return HQ_ERR_SHAPE;
+  if (ld < len || ld >= 2 * kMaxDim) return HQ_ERR_SHAPE;
   const int64_t lds = (t && !tiles) ? q->lds_t : q->lds;
   const int64_t need = tiles ? blocks(q->cols) : (t ? q->cols : q->rows);
   if (lds < need) return HQ_ERR_SHAPE;
