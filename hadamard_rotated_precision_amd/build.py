@@ -13,7 +13,8 @@ SOURCES = ["hq_rotate.hip", "hq_prologue.hip", "hq_gemm.hip", "hq_static.hip", "
            "hq_profile.cpp"]
 # the operators of include/hq_train.h, a library of their own that links libhq.so
 TRAIN_LIB = os.path.join(HERE, "libhq_train.so")
-TRAIN_SOURCES = ["hq_block.hip", "hq_block_gemm.hip", "hq_adamw.hip", "hq_train_api.cpp"]
+TRAIN_SOURCES = ["hq_block.hip", "hq_block_gemm.hip", "hq_block_gemv.hip", "hq_adamw.hip",
+                 "hq_train_api.cpp"]
 
 # -packed-fp32-ops: hipcc forms packed fp32 ops from plain float code; keep them out.
 HIP_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

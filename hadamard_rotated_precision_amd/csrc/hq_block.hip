@@ -38,22 +38,6 @@ struct BlockQuantArgs {
   int vec;   // rows start on 16-byte boundaries and hold whole groups of eight elements
 };
 
-// The scale of a block whose largest magnitude has the bit pattern `a`, and r = 1 / s. A NaN or
-// infinity: s = NaN, r = 0.
-__device__ inline void block_scale(uint32_t a, bool pow2, float& s, float& r) {
-  s = __uint_as_float(a) / 448.0f;   // correctly rounded
-  if (pow2) s = __uint_as_float((__float_as_uint(s) + 0x7FFFFFu) & 0x7F800000u);
-  s = fmaxf(s, 1.17549435e-38f);     // 2^-126: 1 / s stays finite
-  r = 1.0f / s;
-  if (a == 0u) s = 0.0f, r = 0.0f;
-  if (a >= 0x7F800000u) s = __uint_as_float(0x7FC00000u), r = 0.0f;
-}
-
-__device__ inline uint32_t mag(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
-__device__ inline uint32_t shfl_max(uint32_t x, int m) {
-  return max(x, static_cast<uint32_t>(__shfl_xor(static_cast<int>(x), m, 64)));
-}
-
 template <class T, bool TILES>
 __global__ __launch_bounds__(256) void block_quant_kernel(BlockQuantArgs g) {
   constexpr int TP = 144;   // LDS pitch of a transposed code row
@@ -72,18 +56,13 @@ __global__ __launch_bounds__(256) void block_quant_kernel(BlockQuantArgs g) {
 
   uint32_t rm[8], cm[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    rm[i] = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) rm[i] = max(rm[i], mag(v[i][j]));
-  }
+  for (int i = 0; i < 8; ++i) rm[i] = mag8(v[i]);
   float sr[8], rr[8];
   if constexpr (TILES) {
     uint32_t a = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) a = max(a, rm[i]);
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) a = shfl_max(a, m);
+    a = shfl_max(shfl_max(max16(a), 16), 32);
     if ((t & 63) == 0) cmax[wave][0] = a;
     __syncthreads();
     a = max(max(cmax[0][0], cmax[1][0]), max(cmax[2][0], cmax[3][0]));
@@ -95,19 +74,14 @@ __global__ __launch_bounds__(256) void block_quant_kernel(BlockQuantArgs g) {
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-#pragma unroll
-      for (int m = 1; m < 16; m <<= 1) rm[i] = shfl_max(rm[i], m);
-      block_scale(rm[i], g.pow2, sr[i], rr[i]);
+      block_scale(max16(rm[i]), g.pow2, sr[i], rr[i]);
     }
   }
 
   if (g.codes) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      uint2 q;
-      q.x = e4m3_pack4(v[i][0], v[i][1], v[i][2], v[i][3], rr[i]);
-      q.y = e4m3_pack4(v[i][4], v[i][5], v[i][6], v[i][7], rr[i]);
-      if (!(sr[i] == sr[i])) q = {0u, 0u};
+      const uint2 q = e4m3_codes8(v[i], sr[i], rr[i]);
       // zeros up to the next multiple of 16 columns, which the pitch covers
       if (row0 + i < g.rows && col0 < ((g.cols + 15) & ~int64_t{15}))
         *reinterpret_cast<uint2*>(g.codes + (row0 + i) * g.ld + col0) = q;
@@ -139,11 +113,8 @@ __global__ __launch_bounds__(256) void block_quant_kernel(BlockQuantArgs g) {
   }
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    uint2 q;
-    q.x = e4m3_pack4(v[0][j], v[1][j], v[2][j], v[3][j], rc[j]);
-    q.y = e4m3_pack4(v[4][j], v[5][j], v[6][j], v[7][j], rc[j]);
-    if (!(sc[j] == sc[j])) q = {0u, 0u};
-    *reinterpret_cast<uint2*>(&turned[(8 * cg + j) * TP + 8 * rg]) = q;
+    const float u[8] = {v[0][j], v[1][j], v[2][j], v[3][j], v[4][j], v[5][j], v[6][j], v[7][j]};
+    *reinterpret_cast<uint2*>(&turned[(8 * cg + j) * TP + 8 * rg]) = e4m3_codes8(u, sc[j], rc[j]);
   }
   __syncthreads();
   // 8 lanes cover the 128 codes of a transposed row
@@ -157,6 +128,30 @@ __global__ __launch_bounds__(256) void block_quant_kernel(BlockQuantArgs g) {
   }
 }
 
+// ROWS blocks in the row-major layout alone: sixteen lanes take the 128 columns of a block, a
+// thread the same eight columns of R rows (R loads in flight; one where there are few rows).
+template <class T, int R>
+__global__ __launch_bounds__(256) void block_quant_rows_kernel(BlockQuantArgs g) {
+  const int t = threadIdx.x;
+  const int span = (g.tiles_c + 15) >> 4;               // workgroups along a row: 16 blocks each
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x / span) * R;
+  const int64_t col0 = static_cast<int64_t>(blockIdx.x % span) * 2048 + 8 * t;
+  const int64_t n = g.cols - col0;
+  float v[R][8];
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+    load8<T>(g.src, (row0 + i) * g.cols + col0, row0 + i < g.rows ? n : 0, g.vec, v[i]);
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    float s, r;
+    block_scale(max16(mag8(v[i])), g.pow2, s, r);
+    if (row0 + i >= g.rows) continue;
+    if (col0 < ((g.cols + 15) & ~int64_t{15}))
+      *reinterpret_cast<uint2*>(g.codes + (row0 + i) * g.ld + col0) = e4m3_codes8(v[i], s, r);
+    if ((t & 15) == 0 && n > 0) g.scales[(col0 >> 7) * g.lds + row0 + i] = s;
+  }
+}
+
 hipError_t block_quant_pass(const BlockQuantPass& p, hipStream_t st) {
   const int64_t tiles_r = (p.rows + 127) / 128, tiles_c = (p.cols + 127) / 128;
   BlockQuantArgs a{p.src, p.rows, p.cols, p.codes, p.ld, p.codes_t, p.ld_t, p.scales, p.lds,
@@ -165,6 +160,22 @@ hipError_t block_quant_pass(const BlockQuantPass& p, hipStream_t st) {
   const double units = static_cast<double>(p.rows) * p.cols * (bytes + (p.codes != nullptr) + (p.codes_t != nullptr));
   const int tok = prof_open(K_ROT_QUANT, units);
   const dim3 grid(static_cast<unsigned>(tiles_r * tiles_c)), block(256);
+  if (!p.tiles && !p.codes_t) {
+    // four rows a thread once one row a thread would fill the chip twice over
+    const int64_t span = (tiles_c + 15) / 16;
+    const bool many = p.rows * span >= 4096;
+    const dim3 rgrid(static_cast<unsigned>((many ? (p.rows + 3) / 4 : p.rows) * span));
+#define HQ_R(T) \
+  return many ? launch_k(block_quant_rows_kernel<T, 4>, rgrid, block, st, tok, a) \
+              : launch_k(block_quant_rows_kernel<T, 1>, rgrid, block, st, tok, a)
+    switch (p.in_dt) {
+      case DT_F32: HQ_R(F32);
+      case DT_F16: HQ_R(F16);
+      case DT_BF16: HQ_R(BF16);
+    }
+#undef HQ_R
+    return hipErrorInvalidValue;
+  }
 #define HQ_Q(T) \
   return p.tiles ? launch_k(block_quant_kernel<T, true>, grid, block, st, tok, a) \
                  : launch_k(block_quant_kernel<T, false>, grid, block, st, tok, a)

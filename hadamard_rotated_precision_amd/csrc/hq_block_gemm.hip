@@ -28,15 +28,6 @@ struct BlockGemmArgs {
   int accumulate;
 };
 
-// Eight E4M3 codes as fp16 values (exact: E4M3 is a subset of fp16).
-__device__ inline v8h f8_to_h8(uint2 q) {
-  const v2h a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(q.x, 1.0f, false);
-  const v2h b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(q.x, 1.0f, true);
-  const v2h c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(q.y, 1.0f, false);
-  const v2h d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(q.y, 1.0f, true);
-  return v8h{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-}
-
 // ------------------------------------------------------------------ tiled kernel (FP8 instruction)
 // How the scales come in:
 //   S_TILES: p's scale is one number per wave and K step (a wave's P rows lie inside one 128-row
@@ -289,7 +280,7 @@ __global__ __launch_bounds__(64) void block_gemm_plain_kernel(BlockGemmArgs g) {
       uint2 qa = {0u, 0u}, qb = {0u, 0u};
       if (k < K16 && m < g.M) qa = *reinterpret_cast<const uint2*>(pa + k);
       if (k < K16 && n < g.N) qb = *reinterpret_cast<const uint2*>(pb + k);
-      t = __builtin_amdgcn_mfma_f32_32x32x16_f16(f8_to_h8(qb), f8_to_h8(qa), t, 0, 0, 0);
+      t = __builtin_amdgcn_mfma_f32_32x32x16_f16(f8_to_h8(qb.x, qb.y), f8_to_h8(qa.x, qa.y), t, 0, 0, 0);
     }
     const float sa = m < g.M ? g.q.scales[(g.q.tiles ? m / 128 : m) * g.q.sg + kb * g.q.sk] : 0.0f;
 #pragma unroll
@@ -331,6 +322,7 @@ static hipError_t launch_16bit(const BlockGemmPass& p, const BlockGemmArgs& a, h
 }
 
 hipError_t block_gemm_pass(const BlockGemmPass& p, hipStream_t st) {
+  if (p.M <= kBlockGemvRows && p.K > 0) return block_gemv_pass(p, nullptr, 0, false, st);
   BlockGemmArgs a{p.b, p.a, p.M, p.N, p.K, p.c, p.accumulate};
   const int tok = prof_open(K_GEMM, 2.0 * p.M * p.N * p.K);
   const dim3 grid(static_cast<unsigned>(((p.M + 31) / 32) * ((p.N + 31) / 32)));

@@ -1,0 +1,200 @@
+// hq_block_gemv.hip — block-scaled FP8 product for a few output rows (at most 16 tokens):
+//   c[m][n] (+)= sum_kb sa(m,kb) sb(n,kb) sum_{k in kb} a[m][k] b[n][k]
+//
+// What bounds it: the bytes of b, read once. A workgroup takes 16 RT rows of b and the whole
+// contraction; its eight waves take every eighth block of 128 K each, so that together they read
+// 1 KB of every row at a time. A wave's fragments come straight from memory into the operand
+// registers (16 rows x 64 contiguous bytes per load), two blocks ahead of their use; the tokens
+// are the lanes' side of v_mfma_f32_16x16x128_f8f6f4, padded to 16 with zeros. The eight partial
+// sums meet in LDS and are added in the order of the waves.
+//
+// The tokens come as codes, or (fused, for few enough elements) as the caller's own values:
+// then every workgroup quantizes them into LDS while its first rows of b are on their way.
+// Quantizing again in each workgroup costs less than a launch of its own as long as a thread has
+// few elements to do.
+#include "hq_device.hpp"
+#include "hq_launch.hpp"
+#include "hq_train_device.hpp"
+#include "hq_train_internal.hpp"
+
+namespace hq {
+
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+
+constexpr int kGvWaves = 8;
+constexpr int kGvAhead = 2;              // blocks of K in flight per wave
+constexpr int kGvCodes = 32768;          // LDS bytes of the tokens' codes (fused)
+constexpr int kGvFar = 0x7FFFFFF0;
+
+struct GemvArgs {
+  BlockOperand p, q;    // b, and a's codes (not fused)
+  const void* x;        // a's values (fused): M x K, contiguous
+  int M;
+  int64_t N;
+  int K;
+  int x_dt, pow2, wide; // fused: type, scale kind, rows on 16-byte boundaries in whole groups of 8
+  void* c;
+  int accumulate;
+};
+
+// Fused: codes of the tokens in LDS, one thread per eight elements, sixteen lanes per block.
+template <class T>
+__device__ inline void quantize_tokens(const GemvArgs& g, int kpad, uint8_t* codes, float* scales) {
+  const int groups = kpad / 8, kb = kpad / 128;
+  for (int i = threadIdx.x; i < g.M * groups; i += 64 * kGvWaves) {
+    const int m = i / groups, c = 8 * (i - m * groups);
+    float v[8];
+    load8<T>(g.x, static_cast<int64_t>(m) * g.K + c, max(g.K - c, 0), g.wide, v);
+    float s, r;
+    block_scale(max16(mag8(v)), g.pow2, s, r);
+    *reinterpret_cast<uint2*>(codes + m * kpad + c) = e4m3_codes8(v, s, r);
+    if ((threadIdx.x & 15) == 0) scales[m * kb + (c >> 7)] = s;
+  }
+}
+
+// EXACT: the fp16 instruction on the codes' values (fp32 outputs); else the FP8 one.
+template <class Out, int RT, bool P_ROWS, bool EXACT, bool FUSED>
+__global__ __launch_bounds__(64 * kGvWaves) void block_gemv_kernel(GemvArgs g) {
+  __shared__ float part[kGvWaves][RT][64][4];
+  __shared__ __attribute__((aligned(16))) uint8_t xc[FUSED ? kGvCodes : 16];
+  __shared__ float xs[FUSED ? kGvCodes / 128 : 4];
+  const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int lr = lane & 15, lg = lane >> 4;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * (16 * RT);
+  const int rows = static_cast<int>(min<int64_t>(16 * RT, g.N - n0));
+  const int ldp = static_cast<int>(g.p.ld), KB = (g.K + 127) / 128, K16 = (g.K + 15) & ~15, kpad = KB * 128;
+  const __amdgpu_buffer_rsrc_t rsp = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint8_t*>(g.p.codes + n0 * g.p.ld), 0, rows * ldp, kBufferFlags);
+  const __amdgpu_buffer_rsrc_t rsq = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint8_t*>(g.q.codes), 0, FUSED ? 0 : g.M * static_cast<int>(g.q.ld), kBufferFlags);
+
+  // chunks lg and lg + 4 of a row's 128 bytes (for both operands: products pair equal K)
+  auto chunks = [&](const __amdgpu_buffer_rsrc_t& rs, int row_off, int kb) {
+    const int k = kb * 128 + 16 * lg;
+    const v4i a = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rs, k < K16 ? row_off + k : kGvFar, 0, 0));
+    const v4i b = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rs, k + 64 < K16 ? row_off + k + 64 : kGvFar, 0, 0));
+    return v8i{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  };
+  v8i wf[kGvAhead][RT], xf[kGvAhead];
+  float sx[kGvAhead];
+  v4f sw[kGvAhead][RT];
+  auto fetch = [&](int slot, int kb) {
+#pragma unroll
+    for (int i = 0; i < RT; ++i) wf[slot][i] = chunks(rsp, (16 * i + lr) * ldp, kb);
+    const int kc = min(kb, KB - 1);
+    if constexpr (P_ROWS) {
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int64_t n = n0 + 16 * i + 4 * lg + r;
+          sw[slot][i][r] = n < g.N ? g.p.scales[n + kc * g.p.sk] : 0.0f;
+        }
+    } else {
+      sw[slot][0][0] = g.p.scales[(n0 >> 7) * g.p.sg + kc * g.p.sk];
+    }
+    if constexpr (!FUSED) {
+      xf[slot] = chunks(rsq, lr * static_cast<int>(g.q.ld), kb);
+      sx[slot] = lr < g.M ? g.q.scales[(g.q.tiles ? 0 : lr) * g.q.sg + kc * g.q.sk] : 0.0f;
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < kGvAhead; ++s) fetch(s, w + kGvWaves * s);
+
+  if constexpr (FUSED) {
+    switch (g.x_dt) {
+      case DT_F32: quantize_tokens<F32>(g, kpad, xc, xs); break;
+      case DT_F16: quantize_tokens<F16>(g, kpad, xc, xs); break;
+      default: quantize_tokens<BF16>(g, kpad, xc, xs); break;
+    }
+    __syncthreads();
+  }
+
+  v4f acc[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) acc[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  auto block = [&](int slot, int kb) {
+    if constexpr (FUSED) {
+      v4i a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
+      sx[slot] = 0.0f;
+      if (lr < g.M) {
+        const uint8_t* row = xc + lr * kpad + kb * 128 + 16 * lg;
+        a = *reinterpret_cast<const v4i*>(row);
+        b = *reinterpret_cast<const v4i*>(row + 64);
+        sx[slot] = xs[lr * KB + kb];
+      }
+      xf[slot] = v8i{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    }
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const v4f u = multiply_block<EXACT>(wf[slot][i], xf[slot]);
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        acc[i][r] = __builtin_fmaf(u[r], sx[slot] * (P_ROWS ? sw[slot][i][r] : sw[slot][0][0]), acc[i][r]);
+    }
+  };
+  for (int kb = w; kb < KB; kb += kGvWaves * kGvAhead) {
+#pragma unroll
+    for (int s = 0; s < kGvAhead; ++s) {
+      const int k = kb + kGvWaves * s;
+      if (k < KB) {
+        block(s, k);
+        fetch(s, k + kGvWaves * kGvAhead);   // past the end: zeros, never used
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < RT; ++i) *reinterpret_cast<v4f*>(part[w][i][lane]) = acc[i];
+  __syncthreads();
+  for (int e = t; e < g.M * 16 * RT; e += 64 * kGvWaves) {
+    const int m = e / (16 * RT), n = e % (16 * RT);
+    if (n0 + n >= g.N) continue;
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kGvWaves; ++i) sum += part[i][n >> 4][((n & 15) >> 2) * 16 + m][n & 3];
+    const int64_t at = m * g.N + n0 + n;
+    if (g.accumulate) sum += Out::load(g.c, at);
+    put_one<Out>(g.c, at, sum);
+  }
+}
+
+// Fused when the tokens' codes fit their LDS and a thread quantizes at most 16 of its groups of
+// eight elements. Every workgroup repeats that work: past it, a launch of its own is cheaper.
+bool block_gemv_fused_ok(int64_t M, int64_t K) {
+  return M >= 1 && M <= kBlockGemvRows && K >= 1 && M * ((K + 127) / 128 * 128) <= kGvCodes;
+}
+
+template <class Out, int RT, bool P_ROWS, bool EXACT>
+static hipError_t launch_gemv(const GemvArgs& a, bool fused, hipStream_t st, int tok) {
+  const dim3 grid(static_cast<unsigned>((a.N + 16 * RT - 1) / (16 * RT))), block(64 * kGvWaves);
+  return fused ? launch_k(block_gemv_kernel<Out, RT, P_ROWS, EXACT, true>, grid, block, st, tok, a)
+               : launch_k(block_gemv_kernel<Out, RT, P_ROWS, EXACT, false>, grid, block, st, tok, a);
+}
+
+template <class Out, bool EXACT>
+static hipError_t launch_out(const GemvArgs& a, bool fused, hipStream_t st, int tok) {
+  // 32 rows of b per workgroup once that leaves no compute unit without one
+  const bool two = a.N >= 32 * 256;
+  if (!a.p.tiles)
+    return two ? launch_gemv<Out, 2, true, EXACT>(a, fused, st, tok) : launch_gemv<Out, 1, true, EXACT>(a, fused, st, tok);
+  return two ? launch_gemv<Out, 2, false, EXACT>(a, fused, st, tok) : launch_gemv<Out, 1, false, EXACT>(a, fused, st, tok);
+}
+
+hipError_t block_gemv_pass(const BlockGemmPass& p, const void* x, int x_dt, bool pow2, hipStream_t st) {
+  if (p.M < 1 || p.M > kBlockGemvRows || p.K < 1 || (x && !block_gemv_fused_ok(p.M, p.K)))
+    return hipErrorInvalidValue;
+  GemvArgs a{p.b, p.a, x, static_cast<int>(p.M), p.N, static_cast<int>(p.K), x_dt, pow2, p.K % 8 == 0,
+             p.c, p.accumulate};
+  const int tok = prof_open(K_GEMM, 2.0 * p.M * p.N * p.K);
+  switch (p.out_dt) {
+    case DT_F32: return launch_out<F32, true>(a, x != nullptr, st, tok);
+    case DT_F16: return launch_out<F16, false>(a, x != nullptr, st, tok);
+    case DT_BF16: return launch_out<BF16, false>(a, x != nullptr, st, tok);
+  }
+  return hipErrorInvalidValue;
+}
+
+}  // namespace hq

@@ -22,13 +22,13 @@ bool aligned(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p)
 bool valid_dt(int32_t dt) { return dt == HQ_F32 || dt == HQ_F16 || dt == HQ_BF16; }
 size_t dt_bytes(int32_t dt) { return dt == HQ_F32 ? 4 : 2; }
 
-// Largest extent of a matrix axis: tiles are addressed with 32-bit offsets inside a row block,
-// and workgroup counts stay inside a grid.
+// Largest extent of a matrix axis, and 2^38 elements in all: tiles are addressed with 32-bit
+// offsets inside a row block, and workgroup counts stay inside a grid.
 constexpr int64_t kMaxDim = int64_t{1} << 22;
 
 bool dims_ok(int64_t a, int64_t b) {
   return a >= 0 && b >= 0 && a <= kMaxDim && b <= kMaxDim &&
-         blocks(a) * blocks(b) <= (int64_t{1} << 30);
+         blocks(a) * blocks(b) <= (int64_t{1} << 24);
 }
 
 #define HQ_CHECK(expr)             \
@@ -195,6 +195,17 @@ hq_status quantized_product(const void* in, int32_t in_dt, int64_t rows, int64_t
   const size_t own = save ? 0 : scratch_bytes(rows, K);
   HQ_CHECK(check_ws(ws, ws_bytes, own + hq::block_gemm_ws(rows, n, K)));
   HQ_CHECK(stream_ok(stream));
+  if (!save && n > 0 && hq::block_gemv_fused_ok(rows, K)) {
+    BlockGemmPass g;
+    g.b = operand(*w, w_side);
+    g.M = rows;
+    g.N = n;
+    g.K = K;
+    g.c = out;
+    g.out_dt = out_dt;
+    HQ_TRY(hq::block_gemv_pass(g, in, in_dt, scale == HQ_BSCALE_POW2, static_cast<hipStream_t>(stream)));
+    return HQ_OK;
+  }
   hq_block_tensor q = save ? *save : scratch_tensor(ws, rows, K);
   if (rows * K > 0)
     HQ_TRY(hq::block_quant_pass(quant_pass(in, in_dt, rows, K, HQ_BLOCK_ROWS, scale, q),

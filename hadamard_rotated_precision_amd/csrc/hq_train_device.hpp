@@ -78,4 +78,83 @@ __device__ inline void put_run(void* base, int64_t i, int64_t n, const float (&v
   store8<T>(base, i, n, aligned8<T>(base, i), v);
 }
 
+// ---------------------------------------------------------------- block scales and codes
+// Magnitudes are compared as bit patterns: they order like the values, and an infinity or a NaN
+// comes out on top instead of being skipped.
+__device__ inline uint32_t mag(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+__device__ inline uint32_t mag8(const float (&v)[8]) {
+  uint32_t a = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) a = max(a, mag(v[j]));
+  return a;
+}
+__device__ inline uint32_t shfl_max(uint32_t x, int m) {
+  return max(x, static_cast<uint32_t>(__shfl_xor(static_cast<int>(x), m, 64)));
+}
+// Largest of 16 neighbouring lanes, in all of them: quad permutes (lanes ^ 1, ^ 2), then the
+// mirrored half row and row, whose other half or row holds one value already.
+__device__ inline uint32_t max16(uint32_t x) {
+  x = max(x, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), 0xB1, 0xF, 0xF, false)));
+  x = max(x, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), 0x4E, 0xF, 0xF, false)));
+  x = max(x, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), 0x141, 0xF, 0xF, false)));
+  return max(x, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), 0x140, 0xF, 0xF, false)));
+}
+
+// The scale of a block whose largest magnitude has the bit pattern `a`, and r = 1 / s. A NaN or
+// infinity: s = NaN, r = 0.
+__device__ inline void block_scale(uint32_t a, bool pow2, float& s, float& r) {
+  s = __uint_as_float(a) / 448.0f;   // correctly rounded
+  if (pow2) s = __uint_as_float((__float_as_uint(s) + 0x7FFFFFu) & 0x7F800000u);
+  s = fmaxf(s, 1.17549435e-38f);     // 2^-126: 1 / s stays finite
+  r = 1.0f / s;
+  if (a == 0u) s = 0.0f, r = 0.0f;
+  if (a >= 0x7F800000u) s = __uint_as_float(0x7FC00000u), r = 0.0f;
+}
+
+// Four E4M3 codes of v r. |v r| is at most 448 (1 + 2^-22), because s is at least the correctly
+// rounded a / 448, so the hardware conversion (to nearest even, no saturation below 464) needs no
+// clamp.
+__device__ inline uint32_t e4m3_codes4(float a, float b, float c, float d, float r) {
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(a * r, b * r, 0, false);
+  w = __builtin_amdgcn_cvt_pk_fp8_f32(c * r, d * r, w, true);
+  return static_cast<uint32_t>(w);
+}
+// Eight codes; zeros in a block with a NaN scale.
+__device__ inline uint2 e4m3_codes8(const float (&v)[8], float s, float r) {
+  uint2 q;
+  q.x = e4m3_codes4(v[0], v[1], v[2], v[3], r);
+  q.y = e4m3_codes4(v[4], v[5], v[6], v[7], r);
+  return s == s ? q : uint2{0u, 0u};
+}
+
+// ---------------------------------------------------------------- products of one block of K
+// Eight E4M3 codes as fp16 values (exact: E4M3 is a subset of fp16).
+__device__ inline auto f8_to_h8(uint32_t lo, uint32_t hi) {
+  typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+  typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+  const h2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false);
+  const h2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true);
+  const h2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false);
+  const h2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true);
+  return h8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// 16 x 16 products over 128 K. A lane holds 32 of a row's bytes; which ones does not matter as
+// long as both operands agree. EXACT: four fp16 instructions on the codes' values, eight bytes a
+// lane each; else one FP8 instruction.
+template <bool EXACT, class V>
+__device__ inline auto multiply_block(const V& p, const V& q) {
+  typedef float f4 __attribute__((ext_vector_type(4)));
+  f4 u = {0.0f, 0.0f, 0.0f, 0.0f};
+  if constexpr (EXACT) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      u = __builtin_amdgcn_mfma_f32_16x16x32_f16(f8_to_h8(p[2 * i], p[2 * i + 1]),
+                                                 f8_to_h8(q[2 * i], q[2 * i + 1]), u, 0, 0, 0);
+  } else {
+    u = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(p, q, u, 0, 0, 0, 0, 0, 0);
+  }
+  return u;
+}
+
 }  // namespace hq
