@@ -179,13 +179,15 @@ def _blocks(n):
     return (n + B.HQ_BLOCK - 1) // B.HQ_BLOCK
 
 
-def _on(t):
-    """The tensor's device as the current one (a call launches on the current device)."""
-    return torch.cuda.device(t.device)
-
-
-def _stream_of(t, stream):
-    return (torch.cuda.current_stream(t.device) if stream is None else stream).cuda_stream
+def _launch(fn, t, stream, *args):
+    """fn(*args, stream) with t's device current (a call launches on the current device), on the
+    given stream or the device's current one."""
+    dev = t.device.index
+    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if dev == torch.cuda.current_device():
+        return fn(*args, raw)
+    with torch.cuda.device(dev):
+        return fn(*args, raw)
 
 
 def _check_matrix(t, rows, cols, name, device=None):
@@ -267,10 +269,9 @@ class BlockTensor:
     def quantize(self, src, stream=None):
         """hq_block_quantize of src (rows x cols, contiguous) into these buffers."""
         _check_matrix(src, self.rows, self.cols, "src", self.device)
-        with _on(src):
-            B.check(B.hq_block_quantize(ptr(src), HQ_DT[src.dtype], self.rows, self.cols,
-                                        self.shape, self.scale, self.st, _stream_of(src, stream)),
-                    "hq_block_quantize")
+        B.check(_launch(B.hq_block_quantize, src, stream, src.data_ptr(), HQ_DT[src.dtype],
+                        self.rows, self.cols, self.shape, self.scale, self.st),
+                "hq_block_quantize")
         return self
 
     def codes_view(self):
@@ -297,15 +298,13 @@ def block_gemm(a, b, c, a_side=B.HQ_SIDE_ROWS, b_side=B.HQ_SIDE_ROWS, accumulate
     _check_matrix(c, M, N, "c", a.device)
     if b.device != a.device:
         raise ValueError("b is on %s, not on %s" % (b.device, a.device))
-    with _on(c):
-        if ws is None:
-            ws = torch.empty(max(B.hq_block_gemm_workspace_bytes(M, N, K), 16), dtype=torch.uint8,
-                             device=c.device)
-            if stream is not None:
-                ws.record_stream(stream)
-        B.check(B.hq_block_gemm(a.st, a_side, b.st, b_side, ptr(c), HQ_DT[c.dtype],
-                                int(accumulate), ptr(ws), ws.numel(), _stream_of(c, stream)),
-                "hq_block_gemm")
+    if ws is None:
+        ws = torch.empty(max(B.hq_block_gemm_workspace_bytes(M, N, K), 16), dtype=torch.uint8,
+                         device=c.device)
+        if stream is not None:
+            ws.record_stream(stream)
+    B.check(_launch(B.hq_block_gemm, c, stream, a.st, a_side, b.st, b_side, c.data_ptr(),
+                    HQ_DT[c.dtype], int(accumulate), ws.data_ptr(), ws.numel()), "hq_block_gemm")
 
 
 class BlockLayer:
@@ -336,31 +335,27 @@ class BlockLayer:
     def fwd(self, x, y, stream=None):
         _check_matrix(x, self.N, self.C, "x", self.device)
         _check_matrix(y, self.N, self.D, "y", self.device)
-        with _on(x):
-            B.check(B.hq_block_linear_fwd(
-                ptr(x), HQ_DT[x.dtype], self.N, self.C, self.D, self.qw.st, self.scale, ptr(y),
-                HQ_DT[y.dtype], None if self.qx is None else self.qx.st, ptr(self.ws),
-                self.ws_bytes, _stream_of(x, stream)), "hq_block_linear_fwd")
+        B.check(_launch(B.hq_block_linear_fwd, x, stream, x.data_ptr(), HQ_DT[x.dtype], self.N,
+                        self.C, self.D, self.qw.st, self.scale, y.data_ptr(), HQ_DT[y.dtype],
+                        None if self.qx is None else self.qx.st, self.ws.data_ptr(),
+                        self.ws_bytes), "hq_block_linear_fwd")
 
     def bwd_input(self, dy, dx, stream=None):
         _check_matrix(dy, self.N, self.D, "dy", self.device)
         _check_matrix(dx, self.N, self.C, "dx", self.device)
-        with _on(dy):
-            B.check(B.hq_block_linear_bwd_input(
-                ptr(dy), HQ_DT[dy.dtype], self.N, self.C, self.D, self.qw.st, self.scale, ptr(dx),
-                HQ_DT[dx.dtype], None if self.qg is None else self.qg.st, ptr(self.ws),
-                self.ws_bytes, _stream_of(dy, stream)), "hq_block_linear_bwd_input")
+        B.check(_launch(B.hq_block_linear_bwd_input, dy, stream, dy.data_ptr(), HQ_DT[dy.dtype],
+                        self.N, self.C, self.D, self.qw.st, self.scale, dx.data_ptr(),
+                        HQ_DT[dx.dtype], None if self.qg is None else self.qg.st,
+                        self.ws.data_ptr(), self.ws_bytes), "hq_block_linear_bwd_input")
 
     def bwd_weight(self, dw, accumulate=False, stream=None):
         """From the codes that fwd and bwd_input saved."""
         if not self.train:
             raise ValueError("a layer made with train=False saves nothing for the weight gradient")
         _check_matrix(dw, self.D, self.C, "dw", self.device)
-        with _on(dw):
-            B.check(B.hq_block_linear_bwd_weight(
-                self.qg.st, self.qx.st, self.N, self.C, self.D, ptr(dw), HQ_DT[dw.dtype],
-                int(accumulate), ptr(self.ws), self.ws_bytes, _stream_of(dw, stream)),
-                "hq_block_linear_bwd_weight")
+        B.check(_launch(B.hq_block_linear_bwd_weight, dw, stream, self.qg.st, self.qx.st, self.N,
+                        self.C, self.D, dw.data_ptr(), HQ_DT[dw.dtype], int(accumulate),
+                        self.ws.data_ptr(), self.ws_bytes), "hq_block_linear_bwd_weight")
 
 
 class AdamW:
@@ -404,6 +399,7 @@ class AdamW:
         self._scalars = B.hq_adamw_scalars()
         self._device_scalars = None
         self._table = (B.hq_adamw_tensor * len(params))()
+        self._rows = [(self._table[i], p.numel()) for i, p in enumerate(params)]
         for i, (t, p, s) in enumerate(zip(self._table, params, self.states)):
             self._check_state(s, p.numel())
             t.p, t.n, t.weight_decay = ptr(p), p.numel(), decay[i]
@@ -468,24 +464,23 @@ class AdamW:
         """One step with one gradient for each parameter (one dtype for all)."""
         if len(grads) != len(self.params):
             raise ValueError("%d gradients for %d parameters" % (len(grads), len(self.params)))
-        for i, g in enumerate(grads):
-            t = self._table[i]
-            if g.numel() != t.n or not g.is_contiguous() or g.device != self.device:
-                raise ValueError("gradient %d must be contiguous, on %s, with %d elements"
-                                 % (i, self.device, t.n))
-            if g.dtype not in HQ_DT or g.dtype != grads[0].dtype:
-                raise ValueError("gradient %d has dtype %s" % (i, g.dtype))
-            t.grad = g.data_ptr()
-        self.cfg.grad_dtype = HQ_DT[grads[0].dtype]
+        dtype, device = grads[0].dtype, self.device
+        if dtype not in HQ_DT:
+            raise ValueError("gradients have dtype %s: fp32, fp16 or bf16 is needed" % dtype)
+        for g, (row, n) in zip(grads, self._rows):
+            if g.dtype != dtype or g.numel() != n or g.device != device or not g.is_contiguous():
+                raise ValueError("gradients must be contiguous %s tensors on %s with their "
+                                 "parameters' numbers of elements" % (dtype, device))
+            row.grad = g.data_ptr()
+        self.cfg.grad_dtype = HQ_DT[dtype]
         if captured:
             scalars = None
         else:
             scalars = self._scalars
             B.check(B.hq_adamw_scalars_at(self.cfg, self.step_count + 1, grad_scale, scalars),
                     "hq_adamw_scalars_at")
-        with _on(self.params[0]):
-            B.check(B.hq_adamw_step(self._table, len(self.params), self.cfg, scalars,
-                                    ptr(self.device_scalars) if captured else None,
-                                    _stream_of(self.params[0], stream)), "hq_adamw_step")
+        B.check(_launch(B.hq_adamw_step, self.params[0], stream, self._table, len(self.params),
+                        self.cfg, scalars, ptr(self.device_scalars) if captured else None),
+                "hq_adamw_step")
         if not captured:
             self.step_count += 1
