@@ -47,17 +47,18 @@ __device__ inline void lds_dma4(__amdgpu_buffer_rsrc_t rs, float* lds, int voffs
   __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)lds, 4, voffset, 0, 0, 0);
 }
 
-template <class Out, int MODE, int NWP, int NWQ, int TP, int TQ>
-__global__ __launch_bounds__(64 * NWP * NWQ, 1) void block_gemm_kernel(BlockGemmArgs g) {
+template <class Out, int MODE, int NWP, int NWQ, int TP, int TQ, int HOLD, int KS>
+__global__ __launch_bounds__(64 * NWP * NWQ * KS, 2) void block_gemm_kernel(BlockGemmArgs g) {
   constexpr int NW = NWP * NWQ;
   constexpr int BP = NWP * TP * 16, BQ = NWQ * TQ * 16;    // workgroup tile
   constexpr int P_BYTES = BP * 128, Q_BYTES = BQ * 128;
   constexpr int STAGE = P_BYTES + Q_BYTES + (BP + BQ) * 4;
   constexpr int PL = BP / 8 / NW, QL = BQ / 8 / NW;        // 1 KB direct-to-LDS loads per wave
   constexpr int SL = (BP + BQ) / 64;                       // 64-row scale loads of the workgroup
-  static_assert(BP % (8 * NW) == 0 && BQ % (8 * NW) == 0 && SL == NW && BP % 64 == 0 && BQ % 64 == 0, "");
-  __shared__ __attribute__((aligned(16))) int8_t st0[STAGE];
-  __shared__ __attribute__((aligned(16))) int8_t st1[STAGE];
+  static_assert(BP % (8 * NW) == 0 && BQ % (8 * NW) == 0 && SL <= NW && BP % 64 == 0 && BQ % 64 == 0, "");
+  static_assert(HOLD < TP && HOLD <= TQ, "");
+  __shared__ __attribute__((aligned(16))) int8_t st0[KS * STAGE];
+  __shared__ __attribute__((aligned(16))) int8_t st1[KS * STAGE];
 
   // XCD-contiguous order: workgroup b runs on XCD b % 8; each XCD gets consecutive tiles, in
   // groups of 8 q tiles that share p rows in its L2
@@ -72,7 +73,9 @@ __global__ __launch_bounds__(64 * NWP * NWQ, 1) void block_gemm_kernel(BlockGemm
   const int tp = (pid % (kGroup * tiles_p)) / gsize;
   const int64_t p0 = static_cast<int64_t>(tp) * BP, q0 = static_cast<int64_t>(tq) * BQ;
 
-  const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  // KS > 1: groups of waves take every KS-th block of K, in a part of each stage of their own
+  const int kg = KS > 1 ? wave / NW : 0, w = KS > 1 ? wave % NW : wave;
   const int wp = w / NWQ, wq = w % NWQ, lr = lane & 15, lg = lane >> 4;
 
   // operand descriptors from the tile's first row: rows past the end read as zero
@@ -89,10 +92,12 @@ __global__ __launch_bounds__(64 * NWP * NWQ, 1) void block_gemm_kernel(BlockGemm
   const int K16 = static_cast<int>((g.K + 15) & ~int64_t{15});
   const int KT = static_cast<int>((g.K + 127) / 128);
 
-  // scales: each wave fetches those of 64 rows (q's first) for each K step
-  const bool s_is_q = w < BQ / 64;
+  // scales: each wave fetches those of 64 rows (q's first) for each K step; with more waves than
+  // such pieces some are fetched twice, to the same place
+  const int ws = w % SL;
+  const bool s_is_q = ws < BQ / 64;
   const BlockOperand& so = s_is_q ? g.q : g.p;
-  const int64_t s_row0 = s_is_q ? q0 + 64 * w : p0 + 64 * (w - BQ / 64);
+  const int64_t s_row0 = s_is_q ? q0 + 64 * ws : p0 + 64 * (ws - BQ / 64);
   const int64_t s_rows = s_is_q ? g.M : g.N;
   const int64_t s_first = so.tiles ? s_row0 >> 7 : s_row0;                      // group of the first row
   const int64_t s_last = so.tiles ? (s_rows - 1) >> 7 : s_rows - 1;             // of the last valid row
@@ -100,17 +105,24 @@ __global__ __launch_bounds__(64 * NWP * NWQ, 1) void block_gemm_kernel(BlockGemm
   const bool s_in = (so.tiles ? s_row0 + lane < s_rows : s_first + lane <= s_last);
   const float* s_base = so.scales + s_first * so.sg;
 
-  auto dma = [&](int kt, int8_t* stg) {
-    const int k0 = kt * 128;
+  // one of the PL + QL + 1 loads that a wave makes of a stage; bp, bq: its offsets at this K step
+  auto load_piece = [&](int kt, int8_t* stg, int l, unsigned bp, unsigned bq) {
+    if (l == 0) {
+      const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+          const_cast<float*>(s_base + static_cast<int64_t>(min(kt, KT - 1)) * so.sk), 0, 256, kBufferFlags);
+      lds_dma4(rs, reinterpret_cast<float*>(stg + P_BYTES + Q_BYTES) + 64 * ws, s_in ? s_voff : kFar);
+    } else if (l <= QL) {
+      lds_dma16(rsq, stg + P_BYTES + (w + NW * (l - 1)) * 1024, bq + (l - 1) * NW * 8 * ldq);
+    } else {
+      lds_dma16(rsp, stg + (w + NW * (l - 1 - QL)) * 1024, bp + (l - 1 - QL) * NW * 8 * ldp);
+    }
+  };
+  auto dma = [&](int step, int8_t* stg) {
+    const int kt = step * KS + kg, k0 = kt * 128;
     const bool in = kt < KT && k0 + dc < K16;
     const unsigned bp = in ? vp + k0 : kFar, bq = in ? vq + k0 : kFar;
 #pragma unroll
-    for (int i = 0; i < QL; ++i) lds_dma16(rsq, stg + P_BYTES + (w + NW * i) * 1024, bq + i * NW * 8 * ldq);
-#pragma unroll
-    for (int i = 0; i < PL; ++i) lds_dma16(rsp, stg + (w + NW * i) * 1024, bp + i * NW * 8 * ldp);
-    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<float*>(s_base + static_cast<int64_t>(min(kt, KT - 1)) * so.sk), 0, 256, kBufferFlags);
-    lds_dma4(rs, reinterpret_cast<float*>(stg + P_BYTES + Q_BYTES) + 64 * w, s_in ? s_voff : kFar);
+    for (int l = 0; l < PL + QL + 1; ++l) load_piece(kt, stg, l, bp, bq);
   };
   // fragments of v_mfma_f32_16x16x128_f8f6f4: lane group lg holds 32 of the 128 K bytes of row lr;
   // chunks lg and lg + 4, the same for both operands, so products pair equal K whatever the
@@ -119,7 +131,6 @@ __global__ __launch_bounds__(64 * NWP * NWQ, 1) void block_gemm_kernel(BlockGemm
     return join(*reinterpret_cast<const v4i*>(base + lds_at(row, lg)),
                 *reinterpret_cast<const v4i*>(base + lds_at(row, lg + 4)));
   };
-  auto p_frag = [&](const int8_t* stg, int i) { return frag(stg, wp * TP * 16 + i * 16 + lr); };
   auto q_frag = [&](const int8_t* stg, int j) { return frag(stg + P_BYTES, wq * TQ * 16 + j * 16 + lr); };
   auto q_scale = [&](const int8_t* stg, int j) {
     return reinterpret_cast<const float*>(stg + P_BYTES + Q_BYTES)[wq * TQ * 16 + j * 16 + lr];
@@ -131,106 +142,148 @@ __global__ __launch_bounds__(64 * NWP * NWQ, 1) void block_gemm_kernel(BlockGemm
   for (int i = 0; i < TP; ++i)
 #pragma unroll
     for (int j = 0; j < TQ; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-  v8i qf[TQ], pf[2];
-  float f[TQ];          // S_TILES: sp sq; S_ROWS: sq
-  int qe[TQ];           // S_POW2: exponent bytes
 
-  auto load_scales = [&](const int8_t* stg) {
+  // One K step is TP TQ slots, one instruction of 16 x 16 x 128 each, in a fixed order that keeps
+  // the matrix pipe fed: the fma's of a slot follow LAG slots later, when its result is there.
+  // First the rows of tiles 0 .. TP-HOLD-1, reading the fragments of the rows to come; then the
+  // barrier, when every wave's loads of the next stage have landed and its reads of this one are
+  // done; then the HOLD last rows from registers, column by column of tiles: a column's q fragment
+  // is read for the next step as soon as it is free, and the loads of the step after the next go
+  // into this stage's buffer. So nothing of the next step is waited for right after the barrier.
+  constexpr int N = TP * TQ;
+  constexpr int LAG = MODE == S_TILES && N > 8 ? 3 : 2;
+  constexpr int FRONT = (TP - HOLD) * TQ, NDMA = PL + QL + 1;
+  v8i qf[TQ], pf[TP];
+  float f[TQ], fn[TQ], spn = 0.0f;    // S_TILES: sp sq of this step and what the next needs; S_ROWS: sq
+  int qe[TQ];                         // S_POW2: exponent bytes
+  v4f sp[TP];
+  int pe[TP];
+  auto read_p = [&](const int8_t* stg, int i) {
+    pf[i] = frag(stg, wp * TP * 16 + i * 16 + lr);
+    if constexpr (MODE == S_ROWS) sp[i] = *reinterpret_cast<const v4f*>(p_scales(stg) + i * 16 + 4 * lg);
+    if constexpr (MODE == S_POW2) pe[i] = __float_as_int(p_scales(stg)[i * 16 + lr]);
+  };
+  auto read_scales = [&](const int8_t* stg) {
+#pragma unroll
+    for (int j = 0; j < TQ; ++j) fn[j] = q_scale(stg, j);
+    if constexpr (MODE == S_TILES) spn = p_scales(stg)[0];
+  };
+  auto take_scales = [&]() {
 #pragma unroll
     for (int j = 0; j < TQ; ++j) {
-      const float s = q_scale(stg, j);
-      if constexpr (MODE == S_TILES) f[j] = s * p_scales(stg)[0];
-      else if constexpr (MODE == S_ROWS) f[j] = s;
-      else qe[j] = __float_as_int(s) >> 23;
+      if constexpr (MODE == S_POW2) qe[j] = __float_as_int(fn[j]) >> 23;
+      else f[j] = MODE == S_TILES ? fn[j] * spn : fn[j];
     }
   };
-  // row i of tiles against every q tile
-  auto row = [&](const int8_t* stg, int i, const v8i& p) {
-    if constexpr (MODE == S_POW2) {
-      const int pe = __float_as_int(p_scales(stg)[i * 16 + lr]) >> 23;
+  auto slot_i = [](int n) { return n < FRONT ? n / TQ : TP - HOLD + (n - FRONT) % HOLD; };
+  auto slot_j = [](int n) { return n < FRONT ? n % TQ : (n - FRONT) / HOLD; };
+  auto step = [&](int kt, int8_t* cur_, int8_t* nxt_) {
+    int8_t *const cur = cur_ + kg * STAGE, *const nxt = nxt_ + kg * STAGE;
+    v4f u[N];
+    auto finish = [&](int n) {
+      if constexpr (MODE != S_POW2) {
+        const int i = slot_i(n), j = slot_j(n);
 #pragma unroll
-      for (int j = 0; j < TQ; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(p, qf[j], acc[i][j], 0, 0, 0, pe, 0, qe[j]);
-    } else {
-      v4f sp;
-      if constexpr (MODE == S_ROWS) sp = *reinterpret_cast<const v4f*>(p_scales(stg) + i * 16 + 4 * lg);
-#pragma unroll
-      for (int j = 0; j < TQ; ++j) {
-        const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
-        const v4f u = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(p, qf[j], zero, 0, 0, 0, 0, 0, 0);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          if constexpr (MODE == S_TILES) acc[i][j][r] = __builtin_fmaf(u[r], f[j], acc[i][j][r]);
-          else acc[i][j][r] = __builtin_fmaf(u[r], sp[r] * f[j], acc[i][j][r]);
-        }
+        for (int r = 0; r < 4; ++r)
+          acc[i][j][r] = __builtin_fmaf(u[n][r], MODE == S_TILES ? f[j] : sp[i][r] * f[j], acc[i][j][r]);
       }
-    }
-  };
-  // One barrier per K step. Step kt: rows of tiles 0 .. TP-2 with the next row's fragment read
-  // ahead; then this wave's loads of stage kt+1 have landed and its reads of stage kt are done, and
-  // after the barrier everybody's: stage kt's buffer takes the loads of step kt+2 while the last
-  // row of tiles runs and the first fragments of stage kt+1 are read.
-  auto step = [&](int kt, int8_t* cur, int8_t* nxt) {
+    };
+    const int ktn = (kt + 2) * KS + kg, k0 = ktn * 128;
+    const bool in = ktn < KT && k0 + dc < K16;
+    const unsigned bp = in ? vp + k0 : kFar, bq = in ? vq + k0 : kFar;
 #pragma unroll
-    for (int i = 0; i + 1 < TP; ++i) {
-      pf[(i + 1) & 1] = p_frag(cur, i + 1);
-      row(cur, i, pf[i & 1]);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    // the last row's scales come from stage kt too
-    v4f sp_last = {0.0f, 0.0f, 0.0f, 0.0f};
-    int pe_last = 0;
-    if constexpr (MODE == S_ROWS) sp_last = *reinterpret_cast<const v4f*>(p_scales(cur) + (TP - 1) * 16 + 4 * lg);
-    if constexpr (MODE == S_POW2) pe_last = __float_as_int(p_scales(cur)[(TP - 1) * 16 + lr]) >> 23;
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    dma(kt + 2, cur);
-    const v8i p = pf[(TP - 1) & 1];
-#pragma unroll
-    for (int j = 0; j < TQ; ++j) {
+    for (int n = 0; n < N; ++n) {
+      const int i = slot_i(n), j = slot_j(n);
+      if (n == FRONT) {
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+      }
       if constexpr (MODE == S_POW2) {
-        acc[TP - 1][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(p, qf[j], acc[TP - 1][j], 0, 0, 0, pe_last, 0, qe[j]);
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(pf[i], qf[j], acc[i][j], 0, 0, 0, pe[i] >> 23, 0, qe[j]);
       } else {
         const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
-        const v4f u = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(p, qf[j], zero, 0, 0, 0, 0, 0, 0);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          if constexpr (MODE == S_TILES) acc[TP - 1][j][r] = __builtin_fmaf(u[r], f[j], acc[TP - 1][j][r]);
-          else acc[TP - 1][j][r] = __builtin_fmaf(u[r], sp_last[r] * f[j], acc[TP - 1][j][r]);
-        }
+        u[n] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(pf[i], qf[j], zero, 0, 0, 0, 0, 0, 0);
       }
-      qf[j] = q_frag(nxt, j);
+      if (n >= LAG) finish(n - LAG);
+      if (n < FRONT) {
+        // the next row's fragment, and in the last of the front's rows those of the held rows
+        if (n % TQ == 0) read_p(cur, n / TQ + 1);
+        if (n >= FRONT - TQ && n % TQ > 0 && n % TQ < HOLD) read_p(cur, TP - HOLD + n % TQ);
+      } else {
+        const int s = n - FRONT;
+        constexpr int PER = (NDMA + N - FRONT - 1) / (N - FRONT);
+#pragma unroll
+        for (int l = s * PER; l < (s + 1) * PER && l < NDMA; ++l) load_piece(ktn, cur, l, bp, bq);
+        // once row 0's last fma's, which use its scales, are past
+        constexpr int FREE = TQ - 1 + LAG > FRONT ? TQ - 1 + LAG - FRONT : 0;
+        static_assert(FREE < N - FRONT, "");
+        if (s == FREE) read_p(nxt, 0);
+        if (s == 1) read_scales(nxt);
+        if ((s + 1) % HOLD == 0) qf[j] = q_frag(nxt, j);
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
-    pf[0] = p_frag(nxt, 0);
-    load_scales(nxt);
+#pragma unroll
+    for (int n = N - LAG; n < N; ++n) finish(n);
+    take_scales();
   };
-  static_assert(TP % 2 == 0, "row 0's fragment is in pf[0]");
 
-  if (KT > 0) {
-    dma(0, st0);
-    dma(1, st1);
+  const int steps = (KT + KS - 1) / KS;
+  if (steps > 0) {
+    int8_t* const first = st0 + kg * STAGE;
+    dma(0, first);
+    dma(1, st1 + kg * STAGE);
     // the loads of stage 0 have landed: those of stage 1 stay in flight
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(PL + QL + 1) : "memory");
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(NDMA) : "memory");
     __builtin_amdgcn_s_barrier();
 #pragma unroll
-    for (int j = 0; j < TQ; ++j) qf[j] = q_frag(st0, j);
-    pf[0] = p_frag(st0, 0);
-    load_scales(st0);
+    for (int j = 0; j < TQ; ++j) qf[j] = q_frag(first, j);
+    read_p(first, 0);
+    read_scales(first);
+    take_scales();
+    // unrolled over the two stages, each an LDS object of its own: the compiler then waits only
+    // for the loads that a read depends on
     int kt = 0;
-    for (; kt + 1 < KT; kt += 2) {
+    for (; kt + 1 < steps; kt += 2) {
       step(kt, st0, st1);
       step(kt + 1, st1, st0);
     }
-    if (kt < KT) step(kt, st0, st1);
+    if (kt < steps) step(kt, st0, st1);
   }
   // loads past K (zeros) have landed before the stages are used again
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
   __syncthreads();
 
+  // the groups' sums, added in their order by the first
+  if constexpr (KS > 1) {
+    static_assert((KS - 1) * NW * TP * TQ * 1024 <= 2 * KS * STAGE, "");
+    auto at = [&](int group, int i, int j) {
+      const int o = (((group - 1) * NW + w) * TP * TQ + i * TQ + j) * 1024 + lane * 16;
+      return reinterpret_cast<v4f*>(o < KS * STAGE / 1024 * 1024 ? st0 + o : st1 + o - KS * STAGE / 1024 * 1024);
+    };
+#pragma unroll
+    for (int i = 0; i < TP; ++i)
+#pragma unroll
+      for (int j = 0; j < TQ; ++j)
+        if (kg > 0) *at(kg, i, j) = acc[i][j];
+    __syncthreads();
+    if (kg == 0) {
+#pragma unroll
+      for (int e = 1; e < KS; ++e)
+#pragma unroll
+        for (int i = 0; i < TP; ++i)
+#pragma unroll
+          for (int j = 0; j < TQ; ++j) acc[i][j] += *at(e, i, j);
+    }
+    __syncthreads();
+    if (kg > 0) return;
+  }
+
   // Epilogue, a wave alone: a strip of 16 output rows goes through the wave's part of a stage, so
   // that lanes hold eight consecutive outputs of a row and neighbouring lanes continue it.
   constexpr int W = TP * 16, PITCH = W + 4;
-  static_assert(16 * PITCH * 4 * ((NW + 1) / 2) <= STAGE, "the strips of half the waves must fit a stage");
+  static_assert(16 * PITCH * 4 * ((NW + 1) / 2) <= KS * STAGE, "the strips of half the waves must fit a stage");
   float* const strip = reinterpret_cast<float*>((w & 1) ? st1 : st0) + (w >> 1) * 16 * PITCH;
   constexpr int LPR = W / 8, RPI = 64 / LPR;     // lanes per output row, rows per pass
 #pragma unroll
@@ -303,22 +356,55 @@ __global__ __launch_bounds__(64) void block_gemm_plain_kernel(BlockGemmArgs g) {
 
 size_t block_gemm_ws(int64_t, int64_t, int64_t) { return 0; }
 
-template <class Out, int MODE, int NWP, int NWQ, int TP, int TQ>
+template <class Out, int MODE, int NWP, int NWQ, int TP, int TQ, int HOLD, int KS>
 static hipError_t launch_tiled(const BlockGemmArgs& a, hipStream_t st, int tok) {
   constexpr int BP = NWP * TP * 16, BQ = NWQ * TQ * 16;
   const int64_t tiles = ((a.M + BQ - 1) / BQ) * ((a.N + BP - 1) / BP);
-  return launch_k(block_gemm_kernel<Out, MODE, NWP, NWQ, TP, TQ>, dim3(static_cast<unsigned>(tiles)),
-                  dim3(64 * NWP * NWQ), st, tok, a);
+  return launch_k(block_gemm_kernel<Out, MODE, NWP, NWQ, TP, TQ, HOLD, KS>, dim3(static_cast<unsigned>(tiles)),
+                  dim3(64 * NWP * NWQ * KS), st, tok, a);
+}
+
+// Tile size by the time it would take, in microseconds per 128 of K as measured on whole rounds
+// and on ones with fewer workgroups per compute unit (256 x 256: one fits; 128 x 128: two;
+// 64 x 64: four). Large tiles read less from LDS and L2 per product, small ones fill the chip when
+// the output is small: at K = 4096 (us, tiles of 64 / 128 / 256) 256 x 4096 outputs take
+// 11 / 20 / 46, 1000 x 4096 28 / 26 / 48, and 1000 x 13824 at K = 5120 - / 91 / 65.
+static int pick_tile(int64_t M, int64_t N) {
+  constexpr int kCus = 256;
+  struct Shape { int size, fit; double us[4]; };
+  static const Shape shapes[] = {{256, 1, {1.65}}, {128, 2, {0.75, 1.13}}, {64, 4, {0.32, 0.55, 0.72, 0.9}}};
+  int best = 256;
+  double best_us = 0.0;
+  for (const Shape& s : shapes) {
+    const int64_t tiles = ((M + s.size - 1) / s.size) * ((N + s.size - 1) / s.size);
+    const int64_t full = tiles / (kCus * s.fit), rest = (tiles % (kCus * s.fit) + kCus - 1) / kCus;
+    const double us = static_cast<double>(full) * s.us[s.fit - 1] + (rest ? s.us[rest - 1] : 0.0);
+    if (s.size == 256 || us < best_us) best = s.size, best_us = us;
+  }
+  return best;
+}
+
+template <class Out, int MODE>
+static hipError_t launch_mode(const BlockGemmArgs& a, hipStream_t st, int tok) {
+  switch (pick_tile(a.M, a.N)) {
+    case 64: {
+      // two groups of waves over K while no more than two workgroups of eight waves come to a
+      // compute unit (64 x 4096, K = 4096: 9.6 against 10.8 us; 300 x 8192, K = 1024, five tiles
+      // for two units: 10.4 against 8.8)
+      const int64_t tiles = ((a.M + 63) / 64) * ((a.N + 63) / 64);
+      if (tiles <= 512) return launch_tiled<Out, MODE, 2, 2, 2, 2, 1, 2>(a, st, tok);
+      return launch_tiled<Out, MODE, 2, 2, 2, 2, 1, 1>(a, st, tok);
+    }
+    case 128: return launch_tiled<Out, MODE, 2, 2, 4, 4, 2, 1>(a, st, tok);
+    default: return launch_tiled<Out, MODE, 2, 4, 8, 4, MODE == S_POW2 ? 4 : 2, 1>(a, st, tok);
+  }
 }
 
 template <class Out>
 static hipError_t launch_16bit(const BlockGemmPass& p, const BlockGemmArgs& a, hipStream_t st, int tok) {
-  const int mode = (p.a.pow2 && p.b.pow2) ? S_POW2 : (p.b.tiles ? S_TILES : S_ROWS);
-  switch (mode) {
-    case S_TILES: return launch_tiled<Out, S_TILES, 2, 4, 8, 4>(a, st, tok);
-    case S_ROWS: return launch_tiled<Out, S_ROWS, 2, 4, 8, 4>(a, st, tok);
-    default: return launch_tiled<Out, S_POW2, 2, 4, 8, 4>(a, st, tok);
-  }
+  if (p.a.pow2 && p.b.pow2) return launch_mode<Out, S_POW2>(a, st, tok);
+  if (p.b.tiles) return launch_mode<Out, S_TILES>(a, st, tok);
+  return launch_mode<Out, S_ROWS>(a, st, tok);
 }
 
 hipError_t block_gemm_pass(const BlockGemmPass& p, hipStream_t st) {

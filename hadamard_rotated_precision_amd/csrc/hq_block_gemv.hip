@@ -1,11 +1,11 @@
-// hq_block_gemv.hip — block-scaled FP8 product for a few output rows (at most 16 tokens):
+// hq_block_gemv.hip — block-scaled FP8 product for a few output rows (at most 32 tokens):
 //   c[m][n] (+)= sum_kb sa(m,kb) sb(n,kb) sum_{k in kb} a[m][k] b[n][k]
 //
 // What bounds it: the bytes of b, read once. A workgroup takes 16 RT rows of b and the whole
 // contraction; its eight waves take every eighth block of 128 K each, so that together they read
 // 1 KB of every row at a time. A wave's fragments come straight from memory into the operand
 // registers (16 rows x 64 contiguous bytes per load), two blocks ahead of their use; the tokens
-// are the lanes' side of v_mfma_f32_16x16x128_f8f6f4, padded to 16 with zeros. The eight partial
+// are the lanes' side of v_mfma_f32_16x16x128_f8f6f4, padded to 16 or 32 with zeros. The eight partial
 // sums meet in LDS and are added in the order of the waves.
 //
 // The tokens come as codes, or (fused, for few enough elements) as the caller's own values:
@@ -56,9 +56,10 @@ __device__ inline void quantize_tokens(const GemvArgs& g, int kpad, uint8_t* cod
 }
 
 // EXACT: the fp16 instruction on the codes' values (fp32 outputs); else the FP8 one.
-template <class Out, int RT, bool P_ROWS, bool EXACT, bool FUSED>
+template <class Out, int RT, int QT, bool P_ROWS, bool EXACT, bool FUSED>
 __global__ __launch_bounds__(64 * kGvWaves) void block_gemv_kernel(GemvArgs g) {
-  __shared__ float part[kGvWaves][RT][64][4];
+  static_assert(!FUSED || QT == 1, "");
+  __shared__ float part[kGvWaves][RT][QT][64][4];
   __shared__ __attribute__((aligned(16))) uint8_t xc[FUSED ? kGvCodes : 16];
   __shared__ float xs[FUSED ? kGvCodes / 128 : 4];
   const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -68,8 +69,10 @@ __global__ __launch_bounds__(64 * kGvWaves) void block_gemv_kernel(GemvArgs g) {
   const int ldp = static_cast<int>(g.p.ld), KB = (g.K + 127) / 128, K16 = (g.K + 15) & ~15, kpad = KB * 128;
   const __amdgpu_buffer_rsrc_t rsp = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<uint8_t*>(g.p.codes + n0 * g.p.ld), 0, rows * ldp, kBufferFlags);
+  const int rows_q = min(16 * QT, g.M);
+  const int ldq = static_cast<int>(g.q.ld);
   const __amdgpu_buffer_rsrc_t rsq = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<uint8_t*>(g.q.codes), 0, FUSED ? 0 : g.M * static_cast<int>(g.q.ld), kBufferFlags);
+      const_cast<uint8_t*>(g.q.codes), 0, FUSED ? 0 : rows_q * ldq, kBufferFlags);
 
   // chunks lg and lg + 4 of a row's 128 bytes (for both operands: products pair equal K)
   auto chunks = [&](const __amdgpu_buffer_rsrc_t& rs, int row_off, int kb) {
@@ -78,8 +81,8 @@ __global__ __launch_bounds__(64 * kGvWaves) void block_gemv_kernel(GemvArgs g) {
     const v4i b = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rs, k + 64 < K16 ? row_off + k + 64 : kGvFar, 0, 0));
     return v8i{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
   };
-  v8i wf[kGvAhead][RT], xf[kGvAhead];
-  float sx[kGvAhead];
+  v8i wf[kGvAhead][RT], xf[kGvAhead][QT];
+  float sx[kGvAhead][QT];
   v4f sw[kGvAhead][RT];
   auto fetch = [&](int slot, int kb) {
 #pragma unroll
@@ -97,8 +100,12 @@ __global__ __launch_bounds__(64 * kGvWaves) void block_gemv_kernel(GemvArgs g) {
       sw[slot][0][0] = g.p.scales[(n0 >> 7) * g.p.sg + kc * g.p.sk];
     }
     if constexpr (!FUSED) {
-      xf[slot] = chunks(rsq, lr * static_cast<int>(g.q.ld), kb);
-      sx[slot] = lr < g.M ? g.q.scales[(g.q.tiles ? 0 : lr) * g.q.sg + kc * g.q.sk] : 0.0f;
+#pragma unroll
+      for (int j = 0; j < QT; ++j) {
+        const int m = 16 * j + lr;
+        xf[slot][j] = chunks(rsq, (16 * j + lr) * ldq, kb);
+        sx[slot][j] = m < g.M ? g.q.scales[(g.q.tiles ? m >> 7 : m) * g.q.sg + kc * g.q.sk] : 0.0f;
+      }
     }
   };
 #pragma unroll
@@ -113,28 +120,32 @@ __global__ __launch_bounds__(64 * kGvWaves) void block_gemv_kernel(GemvArgs g) {
     __syncthreads();
   }
 
-  v4f acc[RT];
+  v4f acc[RT][QT];
 #pragma unroll
-  for (int i = 0; i < RT; ++i) acc[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int j = 0; j < QT; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
   auto block = [&](int slot, int kb) {
     if constexpr (FUSED) {
       v4i a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
-      sx[slot] = 0.0f;
+      sx[slot][0] = 0.0f;
       if (lr < g.M) {
         const uint8_t* row = xc + lr * kpad + kb * 128 + 16 * lg;
         a = *reinterpret_cast<const v4i*>(row);
         b = *reinterpret_cast<const v4i*>(row + 64);
-        sx[slot] = xs[lr * KB + kb];
+        sx[slot][0] = xs[lr * KB + kb];
       }
-      xf[slot] = v8i{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+      xf[slot][0] = v8i{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
     }
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      const v4f u = multiply_block<EXACT>(wf[slot][i], xf[slot]);
+    for (int i = 0; i < RT; ++i)
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        acc[i][r] = __builtin_fmaf(u[r], sx[slot] * (P_ROWS ? sw[slot][i][r] : sw[slot][0][0]), acc[i][r]);
-    }
+      for (int j = 0; j < QT; ++j) {
+        const v4f u = multiply_block<EXACT>(wf[slot][i], xf[slot][j]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          acc[i][j][r] = __builtin_fmaf(u[r], sx[slot][j] * (P_ROWS ? sw[slot][i][r] : sw[slot][0][0]), acc[i][j][r]);
+      }
   };
   for (int kb = w; kb < KB; kb += kGvWaves * kGvAhead) {
 #pragma unroll
@@ -147,15 +158,17 @@ __global__ __launch_bounds__(64 * kGvWaves) void block_gemv_kernel(GemvArgs g) {
     }
   }
 #pragma unroll
-  for (int i = 0; i < RT; ++i) *reinterpret_cast<v4f*>(part[w][i][lane]) = acc[i];
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int j = 0; j < QT; ++j) *reinterpret_cast<v4f*>(part[w][i][j][lane]) = acc[i][j];
   __syncthreads();
-  for (int e = t; e < g.M * 16 * RT; e += 64 * kGvWaves) {
+  for (int e = t; e < rows_q * 16 * RT; e += 64 * kGvWaves) {
     const int m = e / (16 * RT), n = e % (16 * RT);
     if (n0 + n >= g.N) continue;
     float sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kGvWaves; ++i) sum += part[i][n >> 4][((n & 15) >> 2) * 16 + m][n & 3];
-    const int64_t at = m * g.N + n0 + n;
+    for (int i = 0; i < kGvWaves; ++i) sum += part[i][n >> 4][m >> 4][((n & 15) >> 2) * 16 + (m & 15)][n & 3];
+    const int64_t at = static_cast<int64_t>(m) * g.N + n0 + n;
     if (g.accumulate) sum += Out::load(g.c, at);
     put_one<Out>(g.c, at, sum);
   }
@@ -164,23 +177,31 @@ __global__ __launch_bounds__(64 * kGvWaves) void block_gemv_kernel(GemvArgs g) {
 // Fused when the tokens' codes fit their LDS and a thread quantizes at most 16 of its groups of
 // eight elements. Every workgroup repeats that work: past it, a launch of its own is cheaper.
 bool block_gemv_fused_ok(int64_t M, int64_t K) {
-  return M >= 1 && M <= kBlockGemvRows && K >= 1 && M * ((K + 127) / 128 * 128) <= kGvCodes;
+  return M >= 1 && M <= 16 && K >= 1 && M * ((K + 127) / 128 * 128) <= kGvCodes;
 }
 
-template <class Out, int RT, bool P_ROWS, bool EXACT>
+template <class Out, int RT, int QT, bool P_ROWS, bool EXACT>
 static hipError_t launch_gemv(const GemvArgs& a, bool fused, hipStream_t st, int tok) {
-  const dim3 grid(static_cast<unsigned>((a.N + 16 * RT - 1) / (16 * RT))), block(64 * kGvWaves);
-  return fused ? launch_k(block_gemv_kernel<Out, RT, P_ROWS, EXACT, true>, grid, block, st, tok, a)
-               : launch_k(block_gemv_kernel<Out, RT, P_ROWS, EXACT, false>, grid, block, st, tok, a);
+  const dim3 grid(static_cast<unsigned>((a.N + 16 * RT - 1) / (16 * RT)));
+  const dim3 block(64 * kGvWaves);
+  if constexpr (QT == 1) {
+    if (fused) return launch_k(block_gemv_kernel<Out, RT, QT, P_ROWS, EXACT, true>, grid, block, st, tok, a);
+  }
+  return launch_k(block_gemv_kernel<Out, RT, QT, P_ROWS, EXACT, false>, grid, block, st, tok, a);
+}
+
+template <class Out, bool P_ROWS, bool EXACT>
+static hipError_t launch_rows(const GemvArgs& a, bool fused, hipStream_t st, int tok) {
+  // 32 rows of b per workgroup once that leaves no compute unit without one
+  const bool two = a.N >= 32 * 256;
+  if (a.M <= 16)
+    return two ? launch_gemv<Out, 2, 1, P_ROWS, EXACT>(a, fused, st, tok) : launch_gemv<Out, 1, 1, P_ROWS, EXACT>(a, fused, st, tok);
+  return two ? launch_gemv<Out, 2, 2, P_ROWS, EXACT>(a, fused, st, tok) : launch_gemv<Out, 1, 2, P_ROWS, EXACT>(a, fused, st, tok);
 }
 
 template <class Out, bool EXACT>
 static hipError_t launch_out(const GemvArgs& a, bool fused, hipStream_t st, int tok) {
-  // 32 rows of b per workgroup once that leaves no compute unit without one
-  const bool two = a.N >= 32 * 256;
-  if (!a.p.tiles)
-    return two ? launch_gemv<Out, 2, true, EXACT>(a, fused, st, tok) : launch_gemv<Out, 1, true, EXACT>(a, fused, st, tok);
-  return two ? launch_gemv<Out, 2, false, EXACT>(a, fused, st, tok) : launch_gemv<Out, 1, false, EXACT>(a, fused, st, tok);
+  return a.p.tiles ? launch_rows<Out, false, EXACT>(a, fused, st, tok) : launch_rows<Out, true, EXACT>(a, fused, st, tok);
 }
 
 hipError_t block_gemv_pass(const BlockGemmPass& p, const void* x, int x_dt, bool pow2, hipStream_t st) {

@@ -164,8 +164,26 @@ def test_gemm_accumulates(M, N, K, dtype):
     R.assert_within(c, want, bound, "accumulate")
 
 
+@pytest.mark.parametrize("M,N,K", [(1001, 4100, 260), (1100, 13900, 396), (9000, 1030, 140), (700, 5000, 129),
+                                   (2048, 4096, 640)])
+def test_gemm_large_outputs(M, N, K):
+    """Outputs large enough for the larger tiles, ragged and whole, each way the scales come in."""
+    for k, (dtype, kinds, shapes) in enumerate([
+            (torch.bfloat16, (F32, F32), (ROWS, TILES)), (torch.float16, (POW2, POW2), (ROWS, TILES)),
+            (torch.bfloat16, (F32, F32), (ROWS, ROWS)), (torch.bfloat16, (POW2, POW2), (ROWS, ROWS)),
+            (torch.float32, (F32, F32), (ROWS, ROWS)), (torch.float32, (POW2, POW2), (TILES, TILES))]):
+        print("[case] gemm", M, N, K, dtype, kinds, shapes, flush=True)
+        a, b = operands(M, N, K, kinds, shapes, k)
+        c = draw(gen(1), M, N, dtype)
+        va, vb = as_values(a), as_values(b)
+        want = torch.mm(va, vb.t().contiguous()) + c.double()
+        T.block_gemm(a, b, c, accumulate=True)
+        bound = R.product_bound(va, vb, want, dtype) + 2.0 ** -24 * want.abs()
+        R.assert_within(c, want, bound, "gemm")
+
+
 def test_gemm_leaves_the_memory_around_its_output():
-    for M, N, K in ((5, 77, 200), (130, 131, 140), (257, 300, 300)):
+    for M, N, K in ((5, 77, 200), (130, 131, 140), (257, 300, 300), (1001, 4099, 150), (1101, 13901, 130)):
         a, b = operands(M, N, K, (F32, F32), (ROWS, TILES))
         for dtype in (torch.float32, torch.bfloat16):
             buf = torch.full((M * N + 512,), 3.0, dtype=dtype, device=DEV)
