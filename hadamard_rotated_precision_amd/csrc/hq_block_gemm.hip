@@ -26,6 +26,8 @@ struct BlockGemmArgs {
   int64_t M, N, K;         // q rows, p rows, contraction
   void* c;
   int accumulate;
+  int k_blocks;            // blocks of K per split (grid.y): all of them for one
+  float* part;             // several splits: their sums, M x N each, joined by join_kernel
 };
 
 // ------------------------------------------------------------------ tiled kernel (FP8 instruction)
@@ -91,7 +93,8 @@ __global__ __launch_bounds__(64 * NWP * NWQ * KS, 2) void block_gemm_kernel(Bloc
   const int dr = 8 * w + (lane >> 3), dc = ((lane & 7) ^ ((dr >> 1) & 7)) << 4;
   const int vp = dr * ldp + dc, vq = dr * ldq + dc;
   const int K16 = static_cast<int>((g.K + 15) & ~int64_t{15});
-  const int KT = static_cast<int>((g.K + 127) / 128);
+  // this split's blocks of K
+  const int k_first = blockIdx.y * g.k_blocks, KT = min(static_cast<int>((g.K + 127) / 128), k_first + g.k_blocks);
 
   // scales: each wave fetches those of 64 rows (q's first) for each K step; with more waves than
   // such pieces some are fetched twice, to the same place
@@ -119,7 +122,7 @@ __global__ __launch_bounds__(64 * NWP * NWQ * KS, 2) void block_gemm_kernel(Bloc
     }
   };
   auto dma = [&](int step, int8_t* stg) {
-    const int kt = step * KS + kg, k0 = kt * 128;
+    const int kt = k_first + step * KS + kg, k0 = kt * 128;
     const bool in = kt < KT && k0 + dc < K16;
     const unsigned bp = in ? vp + k0 : kFar, bq = in ? vq + k0 : kFar;
 #pragma unroll
@@ -195,7 +198,7 @@ __global__ __launch_bounds__(64 * NWP * NWQ * KS, 2) void block_gemm_kernel(Bloc
           acc[i][j][r] = __builtin_fmaf(u[n][r], MODE == S_TILES ? f[j] : sp[i][r] * f[j], acc[i][j][r]);
       }
     };
-    const int ktn = (kt + 2) * KS + kg, k0 = ktn * 128;
+    const int ktn = k_first + (kt + 2) * KS + kg, k0 = ktn * 128;
     const bool in = ktn < KT && k0 + dc < K16;
     const unsigned bp = in ? vp + k0 : kFar, bq = in ? vq + k0 : kFar;
 #pragma unroll
@@ -241,7 +244,7 @@ __global__ __launch_bounds__(64 * NWP * NWQ * KS, 2) void block_gemm_kernel(Bloc
     take_scales();
   };
 
-  const int steps = (KT + KS - 1) / KS;
+  const int steps = (KT - k_first + KS - 1) / KS;
   if (steps > 0) {
     int8_t* const first = st0 + kg * STAGE;
     dma(0, first);
@@ -312,6 +315,10 @@ __global__ __launch_bounds__(64 * NWP * NWQ * KS, 2) void block_gemm_kernel(Bloc
       const int64_t m = q0 + wq * TQ * 16 + j * 16 + sr, n = p0 + wp * W + sc;
       if (m < g.M && n < g.N) {
         const int64_t off = m * g.N + n;
+        if (KS > 1 && g.part) {
+          put_run<F32>(g.part + blockIdx.y * g.M * g.N, off, g.N - n, u);
+          continue;
+        }
         if (g.accumulate) {
           float old[8];
           load_run<Out>(g.c, off, g.N - n, old);
@@ -325,13 +332,34 @@ __global__ __launch_bounds__(64 * NWP * NWQ * KS, 2) void block_gemm_kernel(Bloc
   }
 }
 
-size_t block_gemm_ws(int64_t, int64_t, int64_t) { return 0; }
+// c (+)= the splits' sums, added in their order.
+template <class Out>
+__global__ __launch_bounds__(256) void join_kernel(const float* part, int splits, int64_t n, void* c, int accumulate) {
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
+  if (i >= n) return;
+  float sum[8];
+  load_run<F32>(part, i, n - i, sum);
+  for (int s = 1; s < splits; ++s) {
+    float x[8];
+    load_run<F32>(part + s * n, i, n - i, x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[e] += x[e];
+  }
+  if (accumulate) {
+    float old[8];
+    load_run<Out>(c, i, n - i, old);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[e] += old[e];
+  }
+  put_run<Out>(c, i, n - i, sum);
+}
+
 
 template <class Out, int MODE, bool EXACT, int NWP, int NWQ, int TP, int TQ, int HOLD, int KS>
-static hipError_t launch_tiled(const BlockGemmArgs& a, hipStream_t st, int tok) {
+static hipError_t launch_tiled(const BlockGemmArgs& a, hipStream_t st, int tok, int splits = 1) {
   constexpr int BP = NWP * TP * 16, BQ = NWQ * TQ * 16;
   const int64_t tiles = ((a.M + BQ - 1) / BQ) * ((a.N + BP - 1) / BP);
-  return launch_k(block_gemm_kernel<Out, MODE, EXACT, NWP, NWQ, TP, TQ, HOLD, KS>, dim3(static_cast<unsigned>(tiles)),
+  return launch_k(block_gemm_kernel<Out, MODE, EXACT, NWP, NWQ, TP, TQ, HOLD, KS>, dim3(static_cast<unsigned>(tiles), splits),
                   dim3(64 * NWP * NWQ * KS), st, tok, a);
 }
 
@@ -356,16 +384,46 @@ static int pick_tile(int64_t M, int64_t N, bool exact) {
   return best;
 }
 
+// Splits of K over workgroups where 64 x 64 tiles leave most of the chip idle and K is long. With
+// the tiles' two groups of waves a step takes 256 of K: 0.55 us with one workgroup to a compute
+// unit, 1.0 with two; joining costs a launch and the splits' sums, written and read in fp32.
+static int pick_splits(int64_t M, int64_t N, int64_t K) {
+  const int64_t tiles = ((M + 63) / 64) * ((N + 63) / 64), steps = (K + 255) / 256;
+  if (tiles > 256 || steps < 2) return 1;
+  int best = 1;
+  double best_us = 0.0;
+  for (int s = 1; s <= 16 && tiles * s <= 512; ++s) {
+    const double us = static_cast<double>((steps + s - 1) / s) * (tiles * s <= 256 ? 0.55 : 1.0) +
+                      (s > 1 ? 3.0 + static_cast<double>(s) * M * N * 8.0 / 4e6 : 0.0);
+    if (s == 1 || us < best_us) best = s, best_us = us;
+  }
+  // no split without work
+  return static_cast<int>((steps + (steps + best - 1) / best - 1) / ((steps + best - 1) / best));
+}
+
 template <class Out, int MODE, bool EXACT>
-static hipError_t launch_mode(const BlockGemmArgs& a, hipStream_t st, int tok) {
+static hipError_t launch_mode(BlockGemmArgs a, hipStream_t st, int tok) {
+  a.k_blocks = static_cast<int>((a.K + 127) / 128);
   switch (pick_tile(a.M, a.N, EXACT)) {
     case 64: {
       // two groups of waves over K while no more than two workgroups of eight waves come to a
       // compute unit (64 x 4096, K = 4096: 9.6 against 10.8 us; 300 x 8192, K = 1024, five tiles
       // for two units: 10.4 against 8.8)
       const int64_t tiles = ((a.M + 63) / 64) * ((a.N + 63) / 64);
-      if (tiles <= 512) return launch_tiled<Out, MODE, EXACT, 2, 2, 2, 2, 1, 2>(a, st, tok);
-      return launch_tiled<Out, MODE, EXACT, 2, 2, 2, 2, 1, 1>(a, st, tok);
+      if (tiles > 512) return launch_tiled<Out, MODE, EXACT, 2, 2, 2, 2, 1, 1>(a, st, tok);
+      const int splits = pick_splits(a.M, a.N, a.K);
+      if (splits == 1) {
+        a.part = nullptr;
+        return launch_tiled<Out, MODE, EXACT, 2, 2, 2, 2, 1, 2>(a, st, tok);
+      }
+      const int64_t steps = (a.K + 255) / 256;
+      a.k_blocks = 2 * static_cast<int>((steps + splits - 1) / splits);
+      const hipError_t e = launch_tiled<Out, MODE, EXACT, 2, 2, 2, 2, 1, 2>(a, st, tok, splits);
+      if (e != hipSuccess) return e;
+      const int64_t n = a.M * a.N;
+      return launch_k(join_kernel<Out>, dim3(static_cast<unsigned>((n + 2047) / 2048)), dim3(256), st,
+                      prof_open(K_MISC, 4.0 * splits * n), static_cast<const float*>(a.part), splits, n, a.c,
+                      a.accumulate);
     }
     case 128: return launch_tiled<Out, MODE, EXACT, 2, 2, 4, 4, 2, 1>(a, st, tok);
     default:
@@ -373,6 +431,13 @@ static hipError_t launch_mode(const BlockGemmArgs& a, hipStream_t st, int tok) {
         return launch_tiled<Out, MODE, EXACT, 2, 4, 8, 4, MODE == S_POW2 ? 4 : 2, 1>(a, st, tok);
   }
   return hipErrorInvalidValue;
+}
+
+// The splits' sums. The same for every output type: a caller sizes a workspace before it knows.
+size_t block_gemm_ws(int64_t M, int64_t N, int64_t K) {
+  if (M == 0 || N == 0 || K == 0 || block_gemv_ok(M, N, K) || (pick_tile(M, N, false) != 64 && pick_tile(M, N, true) != 64)) return 0;
+  const int splits = pick_splits(M, N, K);
+  return splits > 1 ? static_cast<size_t>(splits) * M * N * sizeof(float) : 0;
 }
 
 template <class Out>
@@ -383,8 +448,9 @@ static hipError_t launch_16bit(const BlockGemmPass& p, const BlockGemmArgs& a, h
 }
 
 hipError_t block_gemm_pass(const BlockGemmPass& p, hipStream_t st) {
-  if (p.M <= kBlockGemvRows && p.K > 0) return block_gemv_pass(p, nullptr, 0, false, st);
-  BlockGemmArgs a{p.b, p.a, p.M, p.N, p.K, p.c, p.accumulate};
+  if (block_gemv_ok(p.M, p.N, p.K)) return block_gemv_pass(p, nullptr, 0, false, st);
+  BlockGemmArgs a{p.b, p.a, p.M, p.N, p.K, p.c, p.accumulate, 0, static_cast<float*>(p.ws)};
+  if (block_gemm_ws(p.M, p.N, p.K) > 0 && !p.ws) return hipErrorInvalidValue;
   const int tok = prof_open(K_GEMM, 2.0 * p.M * p.N * p.K);
   switch (p.out_dt) {
     case DT_F32:   // fp32 results: summed by the fp16 instruction

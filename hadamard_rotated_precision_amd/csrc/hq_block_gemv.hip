@@ -26,7 +26,7 @@ typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 
 constexpr int kGvWaves = 8;
 constexpr int kGvAhead = 2;              // blocks of K in flight per wave
-constexpr int kGvCodes = 32768;          // LDS bytes of the tokens' codes (fused)
+constexpr int kGvCodes = 16384;          // LDS bytes of the tokens' codes (fused)
 constexpr int kGvFar = 0x7FFFFFF0;
 
 struct GemvArgs {
@@ -40,18 +40,32 @@ struct GemvArgs {
   int accumulate;
 };
 
-// Fused: codes of the tokens in LDS, one thread per eight elements, sixteen lanes per block.
+// Fused: codes of the tokens in LDS, a thread per eight elements, sixteen lanes per block, four
+// tokens' loads in flight.
 template <class T>
 __device__ inline void quantize_tokens(const GemvArgs& g, int kpad, uint8_t* codes, float* scales) {
-  const int groups = kpad / 8, kb = kpad / 128;
-  for (int i = threadIdx.x; i < g.M * groups; i += 64 * kGvWaves) {
-    const int m = i / groups, c = 8 * (i - m * groups);
-    float v[8];
-    load8<T>(g.x, static_cast<int64_t>(m) * g.K + c, max(g.K - c, 0), g.wide, v);
+  constexpr int U = 4;
+  auto put = [&](int m, int c, const float (&v)[8]) {
     float s, r;
     block_scale(max16(mag8(v)), g.pow2, s, r);
     *reinterpret_cast<uint2*>(codes + m * kpad + c) = e4m3_codes8(v, s, r);
-    if ((threadIdx.x & 15) == 0) scales[m * kb + (c >> 7)] = s;
+    if ((threadIdx.x & 15) == 0) scales[m * (kpad >> 7) + (c >> 7)] = s;
+  };
+  for (int c = 8 * threadIdx.x; c < kpad; c += 8 * 64 * kGvWaves) {
+    const int n = max(g.K - c, 0);
+    int m = 0;
+    for (; m + U <= g.M; m += U) {
+      float v[U][8];
+#pragma unroll
+      for (int u = 0; u < U; ++u) load8<T>(g.x, static_cast<int64_t>(m + u) * g.K + c, n, g.wide, v[u]);
+#pragma unroll
+      for (int u = 0; u < U; ++u) put(m + u, c, v[u]);
+    }
+    for (; m < g.M; ++m) {
+      float v[8];
+      load8<T>(g.x, static_cast<int64_t>(m) * g.K + c, n, g.wide, v);
+      put(m, c, v);
+    }
   }
 }
 
@@ -174,8 +188,16 @@ __global__ __launch_bounds__(64 * kGvWaves) void block_gemv_kernel(GemvArgs g) {
   }
 }
 
-// Fused when the tokens' codes fit their LDS and a thread quantizes at most 16 of its groups of
-// eight elements. Every workgroup repeats that work: past it, a launch of its own is cheaper.
+// Up to 16 tokens; 17 to 32 while b is small (4096 x 4096 at 17 tokens: 9.7 us against 12.1 on
+// 64 x 64 tiles with K split; 4096 x 11008 at 32: 20.9 against 17.6, each with the tokens'
+// quantization), for the tokens' codes are read again by every workgroup.
+bool block_gemv_ok(int64_t M, int64_t N, int64_t K) {
+  return M >= 1 && K >= 1 && (M <= 16 || (M <= 32 && N * K <= int64_t{1} << 24));
+}
+
+// Fused when the tokens' codes fit their LDS. Every workgroup repeats the quantizing: past that a
+// launch of its own is cheaper (eight tokens of 4096 for 11008 rows: 15.3 us on their own launch,
+// 16.9 fused).
 bool block_gemv_fused_ok(int64_t M, int64_t K) {
   return M >= 1 && M <= 16 && K >= 1 && M * ((K + 127) / 128 * 128) <= kGvCodes;
 }
@@ -192,8 +214,10 @@ static hipError_t launch_gemv(const GemvArgs& a, bool fused, hipStream_t st, int
 
 template <class Out, bool P_ROWS, bool EXACT>
 static hipError_t launch_rows(const GemvArgs& a, bool fused, hipStream_t st, int tok) {
-  // 32 rows of b per workgroup once that leaves no compute unit without one
-  const bool two = a.N >= 32 * 256;
+  // 16 rows of b per workgroup while all workgroups are on the chip at once (three to a compute
+  // unit), else 32: one token at 4096 x 11008 takes 11.5 against 12.6 us, at 5120 x 13824 15.8
+  // against 13.8
+  const bool two = a.N > 16 * 3 * 256;
   if (a.M <= 16)
     return two ? launch_gemv<Out, 2, 1, P_ROWS, EXACT>(a, fused, st, tok) : launch_gemv<Out, 1, 1, P_ROWS, EXACT>(a, fused, st, tok);
   return two ? launch_gemv<Out, 2, 2, P_ROWS, EXACT>(a, fused, st, tok) : launch_gemv<Out, 1, 2, P_ROWS, EXACT>(a, fused, st, tok);
@@ -205,7 +229,7 @@ static hipError_t launch_out(const GemvArgs& a, bool fused, hipStream_t st, int 
 }
 
 hipError_t block_gemv_pass(const BlockGemmPass& p, const void* x, int x_dt, bool pow2, hipStream_t st) {
-  if (p.M < 1 || p.M > kBlockGemvRows || p.K < 1 || (x && !block_gemv_fused_ok(p.M, p.K)))
+  if (!block_gemv_ok(p.M, p.N, p.K) || (x && !block_gemv_fused_ok(p.M, p.K)))
     return hipErrorInvalidValue;
   GemvArgs a{p.b, p.a, x, static_cast<int>(p.M), p.N, static_cast<int>(p.K), x_dt, pow2, p.K % 8 == 0,
              p.c, p.accumulate};

@@ -52,10 +52,10 @@ struct BlockGemmPass {
 size_t block_gemm_ws(int64_t M, int64_t N, int64_t K);
 hipError_t block_gemm_pass(const BlockGemmPass& p, hipStream_t st);
 
-// The product for at most kBlockGemvRows rows of a (hq_block_gemv.hip; block_gemm_pass uses it).
+// The product for few rows of a (hq_block_gemv.hip; block_gemm_pass uses it where block_gemv_ok).
 // x given: a is the M x K matrix x of type x_dt, quantized within (ROWS blocks, scale kind pow2);
 // block_gemv_fused_ok has to hold.
-constexpr int64_t kBlockGemvRows = 32;
+bool block_gemv_ok(int64_t M, int64_t N, int64_t K);
 bool block_gemv_fused_ok(int64_t M, int64_t K);
 hipError_t block_gemv_pass(const BlockGemmPass& p, const void* x, int x_dt, bool pow2, hipStream_t st);
 

@@ -64,6 +64,19 @@ def test_quantize_sizes(rows, cols, shape):
         check_quantized(T.BlockTensor(rows, cols, shape=shape, scale=kind).quantize(x), x, kind)
 
 
+@pytest.mark.parametrize("kind", [F32, POW2])
+def test_quantize_many_scales(kind):
+    """A million blocks of unrelated largest magnitudes: their scales and reciprocals are the
+    correctly rounded ones, or some codes would differ."""
+    x = draw(gen(3), 8192, 16384)
+    x *= torch.exp2(torch.rand(8192, 1, generator=gen(4), device=DEV) * 40 - 20)
+    q = T.BlockTensor(8192, 16384, scale=kind, codes_t=False).quantize(x)
+    for r in range(0, 8192, 1024):
+        want, s = R.quantize(x[r:r + 1024], 1, 128, kind)
+        assert torch.equal(q.codes[r:r + 1024].view(R.E4M3).double(), want)
+        assert torch.equal(q.scales[:, r:r + 1024].double(), s.t())
+
+
 @pytest.mark.parametrize("shape", [ROWS, TILES])
 def test_quantize_one_layout_alone(shape):
     x = draw(gen(5), 200, 333, torch.bfloat16)
@@ -180,6 +193,33 @@ def test_gemm_large_outputs(M, N, K):
         T.block_gemm(a, b, c, accumulate=True)
         bound = R.product_bound(va, vb, want, dtype) + 2.0 ** -24 * want.abs()
         R.assert_within(c, want, bound, "gemm")
+
+
+@pytest.mark.parametrize("M,N,K", [(40, 60, 8192), (300, 200, 5000), (17, 4100, 4200), (64, 2048, 4096), (33, 700, 2049)])
+def test_gemm_long_contractions(M, N, K):
+    """Few outputs and a long contraction: K is split over workgroups and joined."""
+    assert B.hq_block_gemm_workspace_bytes(M, N, K) > 0
+    for k, (dtype, kinds, shapes) in enumerate([
+            (torch.bfloat16, (F32, F32), (ROWS, TILES)), (torch.float16, (POW2, POW2), (ROWS, TILES)),
+            (torch.bfloat16, (F32, F32), (ROWS, ROWS)), (torch.float32, (F32, F32), (ROWS, ROWS))]):
+        a, b = operands(M, N, K, kinds, shapes, k)
+        va, vb = as_values(a), as_values(b)
+        exact = torch.mm(va, vb.t().contiguous())
+        c = torch.empty(M, N, dtype=dtype, device=DEV)
+        T.block_gemm(a, b, c)
+        R.assert_within(c, exact, R.product_bound(va, vb, exact, dtype), "split")
+        c2 = draw(gen(1), M, N, dtype)
+        want = exact + c2.double()
+        T.block_gemm(a, b, c2, accumulate=True)
+        R.assert_within(c2, want, R.product_bound(va, vb, want, dtype) + 2.0 ** -24 * want.abs(), "split, added")
+
+
+def test_gemm_workspace_is_checked():
+    M, N, K = 40, 60, 8192
+    a, b = operands(M, N, K, (F32, F32), (ROWS, TILES))
+    c = torch.empty(M, N, device=DEV)
+    with pytest.raises(B.HQError, match="WORKSPACE"):
+        T.block_gemm(a, b, c, ws=torch.empty(16, dtype=torch.uint8, device=DEV))
 
 
 def test_gemm_leaves_the_memory_around_its_output():
@@ -319,7 +359,7 @@ def test_python_refusals():
         T.BlockLayer(8, 64, 32, weight=T.BlockTensor(32, 64, shape=TILES, codes_t=False)).bwd_input(y, x)
 
 
-STEPS = [(3, 500, 300), (300, 512, 640), (1000, 1030, 778)]
+STEPS = [(3, 500, 300), (300, 512, 640), (1000, 1030, 778), (4000, 200, 300)]
 
 
 class Step:
