@@ -141,8 +141,8 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs g) {
   if (!EIGHT && n == 0) return;
 
   float p[8], gr[8], m[8], v[8];
-  load8<P>(t.p, i, n, true, p);
-  load8<G>(t.grad, i, n, true, gr);
+  load8<P>(t.p, i, n, p);
+  load8<G>(t.grad, i, n, gr);
   if constexpr (EIGHT) {
     const float ms = n > 0 ? t.ms[i >> 7] : 0.0f, vs = n > 0 ? t.vs[i >> 7] : 0.0f;
     e4m3_values(get_codes(t.m, i, n), m);
@@ -154,8 +154,8 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs g) {
       v[j] *= v[j];
     }
   } else {
-    load8<F32>(t.m, i, n, true, m);
-    load8<F32>(t.v, i, n, true, v);
+    load8<F32>(t.m, i, n, m);
+    load8<F32>(t.v, i, n, v);
   }
   const float keep = 1.0f - s.lr * t.wd;
 #pragma unroll
@@ -166,11 +166,11 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs g) {
     const float den = sqrtf(v[j]) * s.inv_sqrt_bias2 + g.eps;
     p[j] = p[j] * keep - s.step_size * m[j] / den;
   }
-  store8<P>(t.p, i, n, true, p);
-  if (t.copy) store8<C>(t.copy, i, n, true, p);
+  store8<P>(t.p, i, n, p);
+  if (t.copy) store8<C>(t.copy, i, n, p);
   if constexpr (!EIGHT) {
-    store8<F32>(t.m, i, n, true, m);
-    store8<F32>(t.v, i, n, true, v);
+    store8<F32>(t.m, i, n, m);
+    store8<F32>(t.v, i, n, v);
   } else {
     float y[8];
 #pragma unroll

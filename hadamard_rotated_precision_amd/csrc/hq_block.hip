@@ -35,7 +35,6 @@ struct BlockQuantArgs {
   int64_t lds_t;
   int tiles_c;
   int pow2;
-  int vec;   // rows start on 16-byte boundaries and hold whole groups of eight elements
 };
 
 // A thread's 8 x 8 elements as they were loaded: 16-bit ones stay packed (32 registers instead of
@@ -43,7 +42,7 @@ struct BlockQuantArgs {
 template <class T, bool WIDE = T::bytes == 4>
 struct Tile8 {
   float d[8][8];
-  __device__ void load(int i, const void* src, int64_t at, int n, bool vec) { load8<T>(src, at, n, vec, d[i]); }
+  __device__ void load(int i, const void* src, int64_t at, int n) { load8<T>(src, at, n, d[i]); }
   __device__ float value(int i, int j) const { return d[i][j]; }
   // largest magnitudes of the rows, and of the columns in pairs (2 q, 2 q + 1), as bit patterns
   __device__ uint32_t row_mag(int i) const { return mag8(d[i]); }
@@ -60,12 +59,10 @@ template <class T>
 struct Tile8<T, false> {
   typedef unsigned short us2 __attribute__((ext_vector_type(2)));
   uint32_t d[8][4];
-  __device__ void load(int i, const void* src, int64_t at, int n, bool vec) {
+  __device__ void load(int i, const void* src, int64_t at, int n) {
     const uint16_t* p = static_cast<const uint16_t*>(src) + at;
-    if (vec) {
-      uint4 q = {0u, 0u, 0u, 0u};
-      if (n >= 8) q = *reinterpret_cast<const uint4*>(p);
-      d[i][0] = q.x; d[i][1] = q.y; d[i][2] = q.z; d[i][3] = q.w;
+    if (n >= 8) {
+      __builtin_memcpy(d[i], p, 16);
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -147,7 +144,7 @@ __global__ __launch_bounds__(256) void block_quant_kernel(BlockQuantArgs g) {
   Tile8<T> x;
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    x.load(i, g.src, (row0 + i) * g.cols + col0, row0 + i < g.rows ? ncol : 0, g.vec);
+    x.load(i, g.src, (row0 + i) * g.cols + col0, row0 + i < g.rows ? ncol : 0);
 
   float rr[8];
   if constexpr (TILES) {
@@ -239,7 +236,7 @@ __global__ __launch_bounds__(256) void block_quant_rows_kernel(BlockQuantArgs g)
   float v[R][8];
 #pragma unroll
   for (int i = 0; i < R; ++i)
-    load8<T>(g.src, (row0 + i) * g.cols + col0, row0 + i < g.rows ? n : 0, g.vec, v[i]);
+    load8<T>(g.src, (row0 + i) * g.cols + col0, row0 + i < g.rows ? n : 0, v[i]);
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     float s, r;
@@ -254,7 +251,7 @@ __global__ __launch_bounds__(256) void block_quant_rows_kernel(BlockQuantArgs g)
 hipError_t block_quant_pass(const BlockQuantPass& p, hipStream_t st) {
   const int64_t tiles_r = (p.rows + 127) / 128, tiles_c = (p.cols + 127) / 128;
   BlockQuantArgs a{p.src, p.rows, p.cols, p.codes, p.ld, p.codes_t, p.ld_t, p.scales, p.lds,
-                   p.scales_t, p.lds_t, static_cast<int>(tiles_c), p.pow2, p.cols % 8 == 0};
+                   p.scales_t, p.lds_t, static_cast<int>(tiles_c), p.pow2};
   const int bytes = p.in_dt == DT_F32 ? 4 : 2;
   const double units = static_cast<double>(p.rows) * p.cols * (bytes + (p.codes != nullptr) + (p.codes_t != nullptr));
   const int tok = prof_open(K_ROT_QUANT, units);

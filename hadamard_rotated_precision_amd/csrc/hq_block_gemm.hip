@@ -316,16 +316,16 @@ __global__ __launch_bounds__(64 * NWP * NWQ * KS, 2) void block_gemm_kernel(Bloc
       if (m < g.M && n < g.N) {
         const int64_t off = m * g.N + n;
         if (KS > 1 && g.part) {
-          put_run<F32>(g.part + blockIdx.y * g.M * g.N, off, g.N - n, u);
+          store8<F32>(g.part + blockIdx.y * g.M * g.N, off, g.N - n, u);
           continue;
         }
         if (g.accumulate) {
           float old[8];
-          load_run<Out>(g.c, off, g.N - n, old);
+          load8<Out>(g.c, off, g.N - n, old);
 #pragma unroll
           for (int e = 0; e < 8; ++e) u[e] += old[e];
         }
-        put_run<Out>(g.c, off, g.N - n, u);
+        store8<Out>(g.c, off, g.N - n, u);
       }
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -338,20 +338,20 @@ __global__ __launch_bounds__(256) void join_kernel(const float* part, int splits
   const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
   if (i >= n) return;
   float sum[8];
-  load_run<F32>(part, i, n - i, sum);
+  load8<F32>(part, i, n - i, sum);
   for (int s = 1; s < splits; ++s) {
     float x[8];
-    load_run<F32>(part + s * n, i, n - i, x);
+    load8<F32>(part + s * n, i, n - i, x);
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum[e] += x[e];
   }
   if (accumulate) {
     float old[8];
-    load_run<Out>(c, i, n - i, old);
+    load8<Out>(c, i, n - i, old);
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum[e] += old[e];
   }
-  put_run<Out>(c, i, n - i, sum);
+  store8<Out>(c, i, n - i, sum);
 }
 
 

@@ -35,7 +35,7 @@ struct GemvArgs {
   int M;
   int64_t N;
   int K;
-  int x_dt, pow2, wide; // fused: type, scale kind, rows on 16-byte boundaries in whole groups of 8
+  int x_dt, pow2;       // fused: type and scale kind
   void* c;
   int accumulate;
 };
@@ -57,13 +57,13 @@ __device__ inline void quantize_tokens(const GemvArgs& g, int kpad, uint8_t* cod
     for (; m + U <= g.M; m += U) {
       float v[U][8];
 #pragma unroll
-      for (int u = 0; u < U; ++u) load8<T>(g.x, static_cast<int64_t>(m + u) * g.K + c, n, g.wide, v[u]);
+      for (int u = 0; u < U; ++u) load8<T>(g.x, static_cast<int64_t>(m + u) * g.K + c, n, v[u]);
 #pragma unroll
       for (int u = 0; u < U; ++u) put(m + u, c, v[u]);
     }
     for (; m < g.M; ++m) {
       float v[8];
-      load8<T>(g.x, static_cast<int64_t>(m) * g.K + c, n, g.wide, v);
+      load8<T>(g.x, static_cast<int64_t>(m) * g.K + c, n, v);
       put(m, c, v);
     }
   }
@@ -231,8 +231,7 @@ static hipError_t launch_out(const GemvArgs& a, bool fused, hipStream_t st, int 
 hipError_t block_gemv_pass(const BlockGemmPass& p, const void* x, int x_dt, bool pow2, hipStream_t st) {
   if (!block_gemv_ok(p.M, p.N, p.K) || (x && !block_gemv_fused_ok(p.M, p.K)))
     return hipErrorInvalidValue;
-  GemvArgs a{p.b, p.a, x, static_cast<int>(p.M), p.N, static_cast<int>(p.K), x_dt, pow2, p.K % 8 == 0,
-             p.c, p.accumulate};
+  GemvArgs a{p.b, p.a, x, static_cast<int>(p.M), p.N, static_cast<int>(p.K), x_dt, pow2, p.c, p.accumulate};
   const int tok = prof_open(K_GEMM, 2.0 * p.M * p.N * p.K);
   switch (p.out_dt) {
     case DT_F32: return launch_out<F32, true>(a, x != nullptr, st, tok);

@@ -178,7 +178,8 @@ def test_gemm_accumulates(M, N, K, dtype):
 
 
 @pytest.mark.parametrize("M,N,K", [(1001, 4100, 260), (1100, 13900, 396), (9000, 1030, 140), (700, 5000, 129),
-                                   (2048, 4096, 640)])
+                                   (2048, 4096, 640),
+                                   (4500, 8300, 200)])
 def test_gemm_large_outputs(M, N, K):
     """Outputs large enough for the larger tiles, ragged and whole, each way the scales come in."""
     for k, (dtype, kinds, shapes) in enumerate([
