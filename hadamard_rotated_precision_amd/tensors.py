@@ -210,6 +210,9 @@ class BlockTensor:
 
     def __init__(self, rows, cols, shape=B.HQ_BLOCK_ROWS, scale=B.HQ_BSCALE_F32, codes=True,
                  codes_t=True, device="cuda"):
+        if not (codes or codes_t):
+            raise ValueError("a BlockTensor holds codes, codes_t or both")
+
         def new(wanted, *size, dtype=torch.float32):
             return torch.empty(size, dtype=dtype, device=device) if wanted else None
 

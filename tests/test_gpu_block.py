@@ -353,6 +353,8 @@ def test_python_refusals():
         with pytest.raises(ValueError):
             layer.fwd(bad, y)
     with pytest.raises(ValueError):
+        T.BlockTensor(8, 64, codes=False, codes_t=False)
+    with pytest.raises(ValueError):
         T.BlockLayer(8, 64, 32, train=False).bwd_weight(torch.zeros(32, 64, device=DEV))
     with pytest.raises(ValueError):
         T.BlockLayer(8, 64, 32, weight=T.BlockTensor(32, 48, shape=TILES))
