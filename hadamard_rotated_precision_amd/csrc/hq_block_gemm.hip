@@ -325,7 +325,7 @@ __global__ __launch_bounds__(64 * NWP * NWQ * KS, 2) void block_gemm_kernel(Bloc
 #pragma unroll
           for (int e = 0; e < 8; ++e) u[e] += old[e];
         }
-        store8<Out>(g.c, off, g.N - n, u);
+        store8_stream<Out>(g.c, off, g.N - n, u);
       }
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");

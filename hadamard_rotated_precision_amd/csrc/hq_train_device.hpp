@@ -65,6 +65,23 @@ __device__ inline void store8(void* base, int64_t i, int64_t n, const float (&v)
   }
 }
 
+// store8 with the non-temporal hint on whole groups (one element aligned, as store8).
+template <class T>
+__device__ inline void store8_stream(void* base, int64_t i, int64_t n, const float (&v)[8]) {
+  typedef uint32_t u4 __attribute__((ext_vector_type(4), aligned(2)));
+  if (n < 8) return store8<T>(base, i, n, v);
+  char* p = static_cast<char*>(base) + i * T::bytes;
+  if constexpr (T::bytes == 4) {
+    __builtin_nontemporal_store(u4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])},
+                                reinterpret_cast<u4*>(p));
+    __builtin_nontemporal_store(u4{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])},
+                                reinterpret_cast<u4*>(p) + 1);
+  } else {
+    __builtin_nontemporal_store(u4{T::pack2(v[0], v[1]), T::pack2(v[2], v[3]), T::pack2(v[4], v[5]), T::pack2(v[6], v[7])},
+                                reinterpret_cast<u4*>(p));
+  }
+}
+
 // ---------------------------------------------------------------- block scales and codes
 // Magnitudes are compared as bit patterns: they order like the values, and an infinity or a NaN
 // comes out on top instead of being skipped.
