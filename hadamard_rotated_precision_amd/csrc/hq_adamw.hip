@@ -82,24 +82,6 @@ __device__ inline void e4m3_values(uint2 q, float (&v)[8]) {
   v[4] = c[0]; v[5] = c[1]; v[6] = d[0]; v[7] = d[1];
 }
 
-// Largest magnitude (as a bit pattern) of the 128 elements of a scale: eight per lane, 16 lanes.
-__device__ inline uint32_t block_mag(const float (&v)[8]) {
-  uint32_t a = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) a = max(a, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-#pragma unroll
-  for (int m = 1; m < 16; m <<= 1)
-    a = max(a, static_cast<uint32_t>(__shfl_xor(static_cast<int>(a), m, 64)));
-  return a;
-}
-
-__device__ inline void state_scale(uint32_t a, float& s, float& r) {
-  s = fmaxf(__uint_as_float(a) / 448.0f, 1.17549435e-38f);
-  r = 1.0f / s;
-  if (a == 0u) s = 0.0f, r = 0.0f;
-  if (a >= 0x7F800000u) s = __uint_as_float(0x7FC00000u), r = 0.0f;
-}
-
 // The E4M3 code of x in [0, 448] below or at it: from the bits for the normal values (x >= 2^-6),
 // in steps of 2^-9 below.
 // m: up when the 20 dropped bits plus 16 random ones (above 4 zeros) carry.
@@ -158,13 +140,17 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs g) {
     load8<F32>(t.v, i, n, v);
   }
   const float keep = 1.0f - s.lr * t.wd;
+  float y[8];     // sqrt(v): the update's, and what 8-bit states store
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const float gj = gr[j] * s.grad_scale;
     m[j] = g.beta1 * m[j] + g.rest1 * gj;
     v[j] = g.beta2 * v[j] + (g.rest2 * gj) * gj;
-    const float den = sqrtf(v[j]) * s.inv_sqrt_bias2 + g.eps;
-    p[j] = p[j] * keep - s.step_size * m[j] / den;
+    y[j] = sqrtf(v[j]);
+    const float den = y[j] * s.inv_sqrt_bias2 + g.eps;
+    // 1 / den to the nearest fp32 (den is at least eps, a normal number); an infinite den keeps 0
+    const float r = den < __builtin_inff() ? reciprocal(den) : __builtin_amdgcn_rcpf(den);
+    p[j] = p[j] * keep - s.step_size * (m[j] * r);
   }
   store8<P>(t.p, i, n, p);
   if (t.copy) store8<C>(t.copy, i, n, p);
@@ -172,15 +158,12 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs g) {
     store8<F32>(t.m, i, n, m);
     store8<F32>(t.v, i, n, v);
   } else {
-    float y[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (j >= n) m[j] = v[j] = 0.0f;   // elements behind the tensor take no part in the maxima
-      y[j] = sqrtf(v[j]);
-    }
+    for (int j = 0; j < 8; ++j)
+      if (j >= n) m[j] = y[j] = 0.0f;   // elements behind the tensor take no part in the maxima
     float ms, mr, vs, vr;
-    state_scale(block_mag(m), ms, mr);
-    state_scale(block_mag(y), vs, vr);
+    block_scale(max16(mag8(m)), false, ms, mr);
+    block_scale(max16(mag8(y)), false, vs, vr);
     if (n == 0) return;
     const uint32_t key = s.key + t.key_add + 0x632BE5ABu * static_cast<uint32_t>(i >> 32);
     uint32_t qm[2] = {0u, 0u}, qv[2] = {0u, 0u};
