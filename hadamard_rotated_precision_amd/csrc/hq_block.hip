@@ -7,14 +7,17 @@
 // magnitudes, and an infinity or a NaN comes out on top instead of being skipped.
 //
 // What bounds it: bytes. R x C elements of e bytes are read once, R C bytes of codes are written
-// for each layout.
+// for each layout: 8192 x 13824 bf16 into both layouts takes 86 to 96 us (4.8 to 5.3 TB/s; a large
+// copy reaches 4.8), 11008 x 4096 fp32 into tiles 55 us (4.9 TB/s).
 //
 // One workgroup of 256 threads takes a 128 x 128 tile, which holds whole blocks of either
 // direction: thread t has columns 8 (t % 16) + [0, 8) of rows 8 (t / 16) + [0, 8) in registers, so
 // the source is read once (16 lanes cover 256 contiguous bytes of a 16-bit row), the row maxima
 // are a reduction over 16 lanes, the column maxima over the eight rows in registers, four lanes
 // and four waves (LDS), and a column's eight codes of a thread pack into two dwords. Those go to
-// LDS and leave as 16-byte pieces of the transposed rows.
+// LDS and leave as 16-byte pieces of the transposed rows. With elements widened in registers and
+// a scale computed by every lane the same pass took 166 us: two workgroups per compute unit and
+// two divisions per row and column in all 16 lanes.
 #include "hq_device.hpp"
 #include "hq_launch.hpp"
 #include "hq_train_device.hpp"

@@ -23,7 +23,10 @@
  *     the same time need workspaces and outputs of their own (two captured graphs too).
  *   - All argument checks run before any launch; on error nothing is launched or written.
  *   - Results do not depend on the order in which workgroups run: the same call on the same data
- *     gives the same bits.
+ *     gives the same bits. They do depend on the shapes: another number of rows may take another
+ *     order of summation.
+ *   - hq_profile_start's kinds: products HQ_KIND_GEMM, quantizing HQ_KIND_ROT_QUANT, the joining of
+ *     a split contraction and AdamW HQ_KIND_MISC.
  */
 #ifndef HQ_TRAIN_H
 #define HQ_TRAIN_H
