@@ -58,7 +58,11 @@ __device__ inline uint32_t mix32(uint32_t h) {
 // Eight code bytes from element i on (bytes past n read as 0 and are not written).
 __device__ inline uint2 get_codes(const void* base, int64_t i, int n) {
   const uint8_t* p = static_cast<const uint8_t*>(base) + i;
-  if (n >= 8) return *reinterpret_cast<const uint2*>(p);
+  if (n >= 8) {
+    uint2 q;
+    __builtin_memcpy(&q, p, 8);
+    return q;
+  }
   uint32_t w[2] = {0u, 0u};
 #pragma unroll
   for (int j = 0; j < 8; ++j)
@@ -69,7 +73,7 @@ __device__ inline uint2 get_codes(const void* base, int64_t i, int n) {
 __device__ inline void put_codes(void* base, int64_t i, int n, uint2 q) {
   uint8_t* p = static_cast<uint8_t*>(base) + i;
   if (n >= 8) {
-    *reinterpret_cast<uint2*>(p) = q;
+    __builtin_memcpy(p, &q, 8);
     return;
   }
   const uint32_t w[2] = {q.x, q.y};

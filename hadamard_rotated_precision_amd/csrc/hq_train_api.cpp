@@ -20,7 +20,8 @@ int64_t blocks(int64_t n) { return (n + HQ_BLOCK - 1) / HQ_BLOCK; }
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 bool aligned(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 bool valid_dt(int32_t dt) { return dt == HQ_F32 || dt == HQ_F16 || dt == HQ_BF16; }
-size_t dt_bytes(int32_t dt) { return dt == HQ_F32 ? 4 : 2; }
+// matrices and vectors of floating-point elements may start at any element
+bool element_aligned(const void* p, int32_t dt) { return aligned(p, dt == HQ_F32 ? 4 : 2); }
 
 // Largest extent of a matrix axis, and 2^38 elements in all: tiles are addressed with 32-bit
 // offsets inside a row block, and workgroup counts stay inside a grid.
@@ -190,7 +191,7 @@ hq_status quantized_product(const void* in, int32_t in_dt, int64_t rows, int64_t
                             void* stream) {
   if (scale != HQ_BSCALE_F32 && scale != HQ_BSCALE_POW2) return HQ_ERR_MODE;
   if ((rows * K > 0 && !in) || (rows * n > 0 && !out)) return HQ_ERR_NULL;
-  if (!aligned(in, 16) || !aligned(out, 16)) return HQ_ERR_ALIGN;
+  if (!element_aligned(in, in_dt) || !element_aligned(out, out_dt)) return HQ_ERR_ALIGN;
   if (save) HQ_CHECK(check_out(save, rows, K, HQ_BLOCK_ROWS, true));
   const size_t own = save ? 0 : scratch_bytes(rows, K);
   HQ_CHECK(check_ws(ws, ws_bytes, own + hq::block_gemm_ws(rows, n, K)));
@@ -229,7 +230,7 @@ hq_status hq_block_quantize(const void* src, int32_t src_dtype, int64_t rows, in
   if (scale != HQ_BSCALE_F32 && scale != HQ_BSCALE_POW2) return HQ_ERR_MODE;
   if (!dims_ok(rows, cols)) return HQ_ERR_SHAPE;
   if (rows * cols > 0 && !src) return HQ_ERR_NULL;
-  if (!aligned(src, 16)) return HQ_ERR_ALIGN;
+  if (!element_aligned(src, src_dtype)) return HQ_ERR_ALIGN;
   HQ_CHECK(check_out(out, rows, cols, shape, false));
   HQ_CHECK(stream_ok(stream));
   if (rows * cols > 0)
@@ -256,7 +257,7 @@ hq_status hq_block_gemm(const hq_block_tensor* a, int32_t a_side, const hq_block
   if ((b_side == HQ_SIDE_ROWS ? b->cols : b->rows) != K) return HQ_ERR_MISMATCH;
   if (!dims_ok(M, N)) return HQ_ERR_SHAPE;
   if (M * N > 0 && !c) return HQ_ERR_NULL;
-  if (!aligned(c, 16)) return HQ_ERR_ALIGN;
+  if (!element_aligned(c, c_dtype)) return HQ_ERR_ALIGN;
   HQ_CHECK(check_ws(ws, ws_bytes, hq::block_gemm_ws(M, N, K)));
   HQ_CHECK(stream_ok(stream));
   return product(operand(*a, a_side), operand(*b, b_side), M, N, K, c, c_dtype, accumulate != 0,
@@ -301,7 +302,7 @@ hq_status hq_block_linear_bwd_weight(const hq_block_tensor* saved_g,
   HQ_CHECK(check_operand(saved_g, HQ_SIDE_COLS, N, D));
   HQ_CHECK(check_operand(saved_x, HQ_SIDE_COLS, N, C));
   if (D * C > 0 && !dw) return HQ_ERR_NULL;
-  if (!aligned(dw, 16)) return HQ_ERR_ALIGN;
+  if (!element_aligned(dw, dw_dtype)) return HQ_ERR_ALIGN;
   HQ_CHECK(check_ws(ws, ws_bytes, hq::block_gemm_ws(D, C, N)));
   HQ_CHECK(stream_ok(stream));
   return product(operand(*saved_g, HQ_SIDE_COLS), operand(*saved_x, HQ_SIDE_COLS), D, C, N, dw,
@@ -365,8 +366,10 @@ hq_status hq_adamw_step(const hq_adamw_tensor* tensors, int32_t count, const hq_
     if (t.n == 0) continue;
     if (!t.p || !t.grad || !t.m || !t.v) return HQ_ERR_NULL;
     if (cfg->state_bits == 8 && (!t.m_scales || !t.v_scales)) return HQ_ERR_NULL;
-    if (!aligned(t.p, 16) || !aligned(t.grad, 16) || !aligned(t.m, 16) || !aligned(t.v, 16) ||
-        !aligned(t.copy, 16) || !aligned(t.m_scales, 4) || !aligned(t.v_scales, 4))
+    const unsigned state = cfg->state_bits == 8 ? 1 : 4;
+    if (!element_aligned(t.p, cfg->param_dtype) || !element_aligned(t.grad, cfg->grad_dtype) ||
+        !element_aligned(t.copy, cfg->copy_dtype) || !aligned(t.m, state) || !aligned(t.v, state) ||
+        !aligned(t.m_scales, 4) || !aligned(t.v_scales, 4))
       return HQ_ERR_ALIGN;
   }
   HQ_CHECK(stream_ok(stream));

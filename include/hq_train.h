@@ -14,8 +14,10 @@
  * Shapes as in hq.h: X is N x C, W is D x C, dY is N x D, row-major and contiguous.
  *
  * Conventions (those of hq.h; where this header adds to them it says so):
- *   - Pointers are DEVICE pointers unless a comment says otherwise, 16-byte aligned
- *     (HQ_ERR_ALIGN). Code pitches are multiples of 16 bytes.
+ *   - Pointers are DEVICE pointers unless a comment says otherwise. Code matrices and workspaces
+ *     are 16-byte aligned and code pitches multiples of 16 bytes; everything else (inputs, outputs,
+ *     scales, parameters, gradients, states) needs only the alignment of its elements
+ *     (HQ_ERR_ALIGN otherwise).
  *   - Every call is asynchronous on `stream`, whose device must be the current one
  *     (HQ_ERR_DEVICE otherwise). No call synchronizes, allocates or records a memset, so all of
  *     them can be captured into a HIP graph.
@@ -65,7 +67,7 @@ typedef enum { HQ_BSCALE_F32 = 0, HQ_BSCALE_POW2 = 1 } hq_block_scale;
  * scales   ROWS:  scales of `codes`: CB x rows, row pitch lds (>= rows);
  *          TILES: of both layouts: RB x CB, row pitch lds (>= CB)
  * scales_t ROWS:  scales of `codes_t`: RB x cols, row pitch lds_t (>= cols); TILES: not used
- * Pitches of scales count floats; scale pointers need only the alignment of a float.
+ * Pitches of scales count floats.
  * Bytes of a code row from its length to the next multiple of 16 are zero (the producer writes
  * them; a caller that brings codes of its own keeps this rule).
  * rows, cols, shape and scale are written by hq_block_quantize and checked by every consumer.
@@ -191,8 +193,7 @@ hq_status hq_adamw_scalars_at(const hq_adamw_config *cfg, int64_t step, double g
 /* One step over `count` tensors (host array, read before the call returns). The step's scalars
  * are those in device memory when device_scalars is given (a captured step reads what it holds at
  * each replay; grad_scale may be written there by a kernel), else those of host_scalars.
- * p, m, v, copy of different tensors must not overlap. Needs the alignment of 16 bytes for p,
- * grad, m, v and copy. No workspace. */
+ * p, m, v, copy and the scales of all tensors must not overlap each other. No workspace. */
 hq_status hq_adamw_step(const hq_adamw_tensor *tensors, int32_t count, const hq_adamw_config *cfg,
                         const hq_adamw_scalars *host_scalars,
                         const hq_adamw_scalars *device_scalars, void *stream);

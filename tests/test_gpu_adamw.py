@@ -284,3 +284,92 @@ def test_training_steps_of_a_block_scaled_layer(bits):
             want, _, _, (bp, _, _) = formula(p0, gr.double(), m, v, step)
             R.assert_within(p, want, stored(want, bp, torch.float32), "p at step %d" % step)
         assert torch.equal(w.view(-1), master.bfloat16())
+
+
+def random_of(seed, step, tensor, element):
+    """The documented random numbers of an element: (for m, for v), each 16 bits."""
+    def mix(h):
+        h ^= h >> 16
+        h = h * 2654435761 & 0xFFFFFFFF
+        h ^= h >> 15
+        h = h * 2891336453 & 0xFFFFFFFF
+        return h ^ h >> 16
+
+    k = mix((seed + 2654435761 * step) & 0xFFFFFFFF) + 0x9E3779B9 * (tensor + 1)
+    u = mix((element & 0xFFFFFFFF) ^ (k + 0x632BE5AB * (element >> 32) & 0xFFFFFFFF))
+    return u & 0xFFFF, u >> 16
+
+
+def check_rounding(st, lo, m, v, seed, step, tensor):
+    """States of elements lo, lo + 1, ... (64-bit m, v) are rounded as the random numbers say, where
+    they are not next to the border."""
+    at = torch.arange(lo, lo + m.numel(), device=DEV) // 128
+    tested = 0
+    for name, exact, which in (("m", m.abs(), 0), ("v", v.sqrt(), 1)):
+        x = (exact / st[name + "_scales"].double()[at]).clamp(max=448)
+        low, high = neighbours(x)
+        share = ((x - low) / (high - low) if name == "m"
+                 else (x * x - low * low) / (high * high - low * low))
+        got = st[name][lo:lo + m.numel()].view(R.E4M3).double().abs()
+        for i in range(m.numel()):
+            u = random_of(seed, step, tensor, lo + i)[which] / 65536
+            edge = 1 - float(share[i])
+            up = u >= edge if name == "m" else u < float(share[i])
+            if min(abs(u - edge), abs(u - float(share[i])), float(share[i]), edge) < 1e-3 or float(x[i]) < 2.0 ** -6:
+                continue
+            assert float(got[i]) == float(high[i] if up else low[i]), (name, lo + i)
+            tested += 1
+    assert tested > m.numel()
+
+
+def test_rounding_follows_the_documented_random_numbers():
+    g = gen(5)
+    params = [randn(g, n, 0.02) for n in (50, 400)]
+    grads = [randn(g, n, 1e-3) for n in (50, 400)]
+    opt = T.AdamW(params, state_bits=8, seed=77, steps_done=8, **HYPER)
+    opt.step(grads)
+    for k in (0, 1):
+        gr = grads[k].double()
+        check_rounding(opt.states[k], 0, 0.1 * gr, 0.05 * gr * gr, 77, 9, k)
+
+
+def test_more_elements_than_32_bits():
+    """2^32 + 1500 elements: the parameters and the states past every 32-bit border."""
+    n = 2 ** 32 + 1500
+    p = torch.full((n,), 0.5, dtype=torch.bfloat16, device=DEV)
+    grad = torch.empty(n, dtype=torch.bfloat16, device=DEV).normal_(generator=gen(1))
+    opt = T.AdamW([p], state_bits=8, seed=3, lr=1e-1, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.1)
+    opt.step([grad])
+    st = opt.states[0]
+    for lo in (2 ** 31 - 512, 2 ** 32 - 512, n - 1024):
+        hi = min(lo + 1024, n)
+        gr = grad[lo:hi].double()
+        want, m, v, (bp, _, _) = formula(torch.full_like(gr, 0.5), gr, torch.zeros_like(gr),
+                                         torch.zeros_like(gr), 1, lr=1e-1)
+        R.assert_within(p[lo:hi], want, stored(want, bp, torch.bfloat16), "p")
+        check_rounding(st, lo, m, v, 3, 1, 0)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_tensors_at_any_element(bits):
+    """Parameters, gradients, copies and states that are pieces of flat buffers, at odd places."""
+    n, sizes = 5000, [1, 130, 2049, 77, 2743]
+    g = gen(2)
+    p, grad = randn(g, n, 0.02), randn(g, n, 1e-3).bfloat16()
+    flat = {k: (torch.zeros(n, device=DEV) if bits == 32 else torch.zeros(n, dtype=torch.uint8, device=DEV)) for k in "mv"}
+    flat["p"], flat["copy"], flat["g"] = p.clone(), torch.zeros(n, dtype=torch.float16, device=DEV), grad
+    cut = lambda t: list(t.split(sizes))  # noqa: E731
+    scales = {k: [torch.zeros(-(-s // 128), device=DEV) for s in sizes] for k in ("m_scales", "v_scales")}
+    states = [dict(m=m, v=v, m_scales=a, v_scales=b) for m, v, a, b in
+              zip(cut(flat["m"]), cut(flat["v"]), scales["m_scales"], scales["v_scales"])]
+    one = T.AdamW(cut(flat["p"]), state_bits=bits, copies=cut(flat["copy"]), states=states, seed=1, **HYPER)
+    other_p = [t.clone() for t in cut(p)]
+    other = T.AdamW(other_p, state_bits=bits, copies=[torch.zeros_like(t, dtype=torch.float16) for t in other_p],
+                    seed=1, **HYPER)
+    for _ in range(2):
+        one.step(cut(flat["g"]))
+        other.step([t.clone() for t in cut(grad)])
+    assert torch.equal(flat["p"], torch.cat(other_p))
+    assert torch.equal(flat["copy"], torch.cat(other.copies))
+    for k in "mv":
+        assert torch.equal(flat[k], torch.cat([s[k] for s in other.states]))

@@ -13,7 +13,7 @@ import pytest
 from hadamard_rotated_precision_amd import binding as B
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
-FAKE, MIS = 0x10000, 0x10004
+FAKE, MIS, ODD = 0x10000, 0x10004, 0x10001
 
 
 def test_every_declared_symbol_is_exported():
@@ -68,7 +68,8 @@ TILES = B.HQ_BLOCK_TILES
     (dict(rows=-1), "HQ_ERR_SHAPE"),
     (dict(cols=1 << 23), "HQ_ERR_SHAPE"),
     (dict(src=None), "HQ_ERR_NULL"),
-    (dict(src=MIS), "HQ_ERR_ALIGN"),
+    (dict(src=ODD), "HQ_ERR_ALIGN"),
+    (dict(src=MIS), "HQ_ERR_DEVICE"),       # elements may start anywhere
     (dict(out=None), "HQ_ERR_NULL"),
     (dict(out=dict(codes=None, codes_t=None)), "HQ_ERR_NULL"),
     (dict(out=dict(scales=None)), "HQ_ERR_NULL"),
@@ -99,7 +100,7 @@ def test_quantize_refusals(kw, want):
 @pytest.mark.parametrize("a,b,kw,want", [
     ({}, {}, {}, "HQ_ERR_DEVICE"),
     ({}, {}, dict(c=None), "HQ_ERR_NULL"),
-    ({}, {}, dict(c=MIS), "HQ_ERR_ALIGN"),
+    ({}, {}, dict(c=FAKE + 2), "HQ_ERR_ALIGN"),
     ({}, {}, dict(dt=5), "HQ_ERR_DTYPE"),
     ({}, {}, dict(a_side=2), "HQ_ERR_MODE"),
     (dict(shape=3), {}, {}, "HQ_ERR_MODE"),
@@ -137,7 +138,7 @@ def fwd(**kw):
     (dict(w=bt(96, 240, TILES)), "HQ_ERR_MISMATCH"),
     (dict(w=bt(96, 256, TILES, codes=None)), "HQ_ERR_NULL"),
     (dict(scale=2), "HQ_ERR_MODE"),
-    (dict(x=MIS), "HQ_ERR_ALIGN"), (dict(y=MIS), "HQ_ERR_ALIGN"),
+    (dict(x=ODD), "HQ_ERR_ALIGN"), (dict(y=ODD), "HQ_ERR_ALIGN"),
     (dict(save=bt(64, 256, codes=None)), "HQ_ERR_NULL"),
     (dict(save=bt(64, 256, ld=128)), "HQ_ERR_SHAPE"),
     (dict(save=None, ws=None), "HQ_ERR_WORKSPACE"),
@@ -170,7 +171,7 @@ def test_backward_refusals():
 
     assert dw() == "HQ_ERR_DEVICE"
     assert dw(dt=4) == "HQ_ERR_DTYPE"
-    assert dw(dw=None) == "HQ_ERR_NULL" and dw(dw=MIS) == "HQ_ERR_ALIGN"
+    assert dw(dw=None) == "HQ_ERR_NULL" and dw(dw=FAKE + 2) == "HQ_ERR_ALIGN"
     assert dw(g=bt(32, 96)) == "HQ_ERR_MISMATCH" and dw(x=bt(64, 240)) == "HQ_ERR_MISMATCH"
     assert dw(g=bt(64, 96, codes_t=None)) == "HQ_ERR_NULL"
     assert dw(x=bt(64, 256, scales_t=None)) == "HQ_ERR_NULL"
@@ -214,7 +215,9 @@ def adamw_step(cfg=None, scalars=True, count=1, device=None, **kw):
     (dict(count=-1), "HQ_ERR_SHAPE"),
     (dict(p=None), "HQ_ERR_NULL"), (dict(grad=None), "HQ_ERR_NULL"),
     (dict(m=None), "HQ_ERR_NULL"), (dict(v_scales=None), "HQ_ERR_NULL"),
-    (dict(p=MIS), "HQ_ERR_ALIGN"), (dict(copy=MIS), "HQ_ERR_ALIGN"),
+    (dict(p=FAKE + 2), "HQ_ERR_ALIGN"), (dict(copy=ODD), "HQ_ERR_ALIGN"),
+    (dict(m=ODD, v=ODD), "HQ_ERR_DEVICE"),      # 8-bit codes
+    (dict(cfg=adamw_cfg(state_bits=32), m=FAKE + 2), "HQ_ERR_ALIGN"),
     (dict(m_scales=FAKE + 2), "HQ_ERR_ALIGN"),
     (dict(n=-1), "HQ_ERR_SHAPE"),
     (dict(weight_decay=-0.1), "HQ_ERR_MODE"), (dict(weight_decay=float("nan")), "HQ_ERR_MODE"),
