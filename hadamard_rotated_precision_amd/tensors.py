@@ -232,10 +232,12 @@ class BlockTensor:
         st.codes, st.codes_t = ptr(codes), ptr(codes_t)
         st.scales, st.scales_t = ptr(scales), ptr(scales_t)
         st.rows, st.cols, st.shape, st.scale = rows, cols, shape, scale
-        st.ld = 0 if codes is None else codes.stride(0)
-        st.ld_t = 0 if codes_t is None else codes_t.stride(0)
-        st.lds = 0 if scales is None else scales.stride(0)
-        st.lds_t = 0 if scales_t is None else scales_t.stride(0)
+        st.ld, st.ld_t, st.lds, st.lds_t = (self._pitch(t) for t in (codes, codes_t, scales, scales_t))
+
+    @staticmethod
+    def _pitch(t):
+        """Elements between rows (a single row's stride means nothing)."""
+        return 0 if t is None else t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
     @classmethod
     def wrap(cls, codes, scales, rows, cols, shape=B.HQ_BLOCK_TILES, scale=B.HQ_BSCALE_F32,
@@ -254,13 +256,19 @@ class BlockTensor:
                       ("scales_t", scales_t, _blocks(rows), cols, torch.float32)]
         for name, t, r, c, dtype in parts:
             if t is None:
+                if name in ("codes", "scales"):
+                    raise ValueError("%s is needed" % name)
                 continue
             if t.dtype != dtype or t.dim() != 2 or t.shape[0] != r or t.shape[1] < c:
                 raise ValueError("%s must be a %s tensor of at least %d x %d" % (name, dtype, r, c))
             if t.stride(1) != 1 and t.shape[1] > 1:
                 raise ValueError("%s must have contiguous rows" % name)
-            if t.device != codes.device:
-                raise ValueError("%s is on %s, not on %s" % (name, t.device, codes.device))
+            if t.device != scales.device:
+                raise ValueError("%s is on %s, not on %s" % (name, t.device, scales.device))
+            if dtype == torch.uint8 and r and c:   # whole 16-byte pieces of the last row are read
+                end = t.storage_offset() + (r - 1) * cls._pitch(t) + pitch16(c)
+                if end > t.untyped_storage().nbytes():
+                    raise ValueError("%s: the last row must reach to the next multiple of 16 bytes" % name)
         for t in (scales, scales_t):
             if scale == B.HQ_BSCALE_POW2 and t is not None and t.numel():
                 mantissa, _ = torch.frexp(t)

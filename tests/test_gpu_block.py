@@ -459,3 +459,129 @@ def test_one_row_of_a_batch_does_not_depend_on_the_others():
     x2[20:] = 0
     T.BlockLayer(40, C, D, weight=w, train=False).fwd(x2, y2)
     assert torch.equal(y[:20], y2[:20]) and not y2[20:].any()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+def test_inputs_and_outputs_at_any_element(dtype):
+    """Views that start at odd elements give the bits of aligned copies."""
+    def odd(x):
+        buf = torch.zeros(x.numel() + 9, dtype=x.dtype, device=DEV)
+        v = buf[3:3 + x.numel()].view(x.shape)
+        return v.copy_(x)
+
+    for N, C, D in ((1, 300, 77), (5, 1000, 256), (40, 129, 300), (300, 512, 640)):
+        g = gen(N)
+        x, w, dy = draw(g, N, C, dtype), draw(g, D, C, dtype, 0.02), draw(g, N, D, dtype)
+        got = []
+        for move in (lambda t: t, odd):
+            layer = T.BlockLayer(N, C, D)
+            y, dx, dw = (move(torch.zeros(s, dtype=dtype, device=DEV)) for s in ((N, D), (N, C), (D, C)))
+            layer.set_weight(move(w))
+            layer.fwd(move(x), y)
+            layer.bwd_input(move(dy), dx)
+            layer.bwd_weight(dw, accumulate=True)
+            y2 = move(torch.zeros_like(y))
+            T.BlockLayer(N, C, D, weight=layer.qw, train=False).fwd(move(x), y2)
+            got.append([t.clone() for t in (y, dx, dw, y2, layer.qx.codes, layer.qx.codes_t)])
+        for a, b in zip(*got):
+            assert torch.equal(a, b)
+
+
+def test_outputs_of_another_type_and_row_scaled_weights():
+    """bf16 tokens with fp32 outputs, and weights in ROWS blocks, for each form of the product."""
+    for N, C, D in ((1, 512, 300), (13, 2000, 130), (60, 300, 700)):
+        x, w, dy = draw(gen(1), N, C, torch.bfloat16), draw(gen(2), D, C, torch.bfloat16, 0.02), draw(gen(3), N, D, torch.bfloat16)
+        for shape, rows in ((TILES, 128), (ROWS, 1)):
+            qw = T.BlockTensor(D, C, shape=shape).quantize(w)
+            for train in (False, True):
+                layer = T.BlockLayer(N, C, D, weight=qw, train=train)
+                y, dx = torch.empty(N, D, device=DEV), torch.empty(N, C, device=DEV)
+                layer.fwd(x, y)
+                layer.bwd_input(dy, dx)
+                for got, a, b in ((y, R.values(x, 1, 128), R.values(w, rows, 128)),
+                                  (dx, R.values(dy, 1, 128), R.values(w, 128, 128 if rows > 1 else 1).t().contiguous())):
+                    want = torch.mm(a, b.t().contiguous())
+                    R.assert_within(got, want, R.product_bound(a, b, want, torch.float32), "fp32")
+
+
+def test_no_tokens():
+    layer = T.BlockLayer(0, 64, 32)
+    layer.set_weight(draw(gen(1), 32, 64))
+    x, y = torch.empty(0, 64, device=DEV), torch.empty(0, 32, device=DEV)
+    layer.fwd(x, y)
+    layer.bwd_input(y, x)
+    dw = torch.full((32, 64), 3.0, device=DEV)
+    layer.bwd_weight(dw, accumulate=True)
+    assert (dw == 3).all()
+    layer.bwd_weight(dw)
+    assert (dw == 0).all()
+
+
+def test_wrapped_rows_and_refusals_of_short_buffers():
+    x = draw(gen(1), 20, 300, torch.bfloat16)
+    q = T.BlockTensor(20, 300).quantize(x)
+    w = T.BlockTensor(50, 300, shape=TILES).quantize(draw(gen(2), 50, 300))
+    scales = torch.full((3, 33), float("nan"), device=DEV)
+    scales[:, :20] = q.scales
+    a = T.BlockTensor.wrap(q.codes, scales, 20, 300, shape=ROWS)
+    c, c2 = torch.empty(20, 50, device=DEV), torch.empty(20, 50, device=DEV)
+    T.block_gemm(q, w, c)
+    T.block_gemm(a, w, c2)
+    assert torch.equal(c, c2)
+    one = T.BlockTensor.wrap(q.codes[:1], q.scales[:, :1].contiguous(), 1, 300, shape=ROWS)   # one row
+    c1 = torch.empty(1, 50, device=DEV)
+    T.block_gemm(one, w, c1)
+    assert torch.allclose(c1, c[:1], rtol=1e-5, atol=1e-6)
+    short = torch.zeros(19 * 304 + 300, dtype=torch.uint8, device=DEV).as_strided((20, 300), (304, 1))
+    with pytest.raises(ValueError, match="multiple of 16"):
+        T.BlockTensor.wrap(short, q.scales, 20, 300, shape=ROWS)
+    with pytest.raises(ValueError):
+        T.BlockTensor.wrap(None, q.scales, 20, 300, shape=ROWS)
+
+
+def test_shared_weights_on_two_streams():
+    w = T.BlockTensor(900, 700, shape=TILES).quantize(draw(gen(1), 900, 700, torch.bfloat16, 0.02))
+    parts = []
+    for n in (3, 200):
+        x = draw(gen(n), n, 700, torch.bfloat16)
+        y = torch.empty(n, 900, dtype=torch.bfloat16, device=DEV)
+        layer = T.BlockLayer(n, 700, 900, weight=w, train=False)
+        layer.fwd(x, y)
+        torch.cuda.synchronize()
+        parts.append((layer, x, y, y.clone(), torch.cuda.Stream()))
+    for rep in range(3):
+        for layer, x, y, _, _ in parts:
+            y.zero_()
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for layer, x, y, _, s in parts:
+                layer.fwd(x, y, s)
+        torch.cuda.synchronize()
+        for _, _, y, want, _ in parts:
+            assert torch.equal(y, want)
+
+
+def test_offsets_past_32_bits():
+    """A matrix of more than 2^31 elements: its last rows and columns, in both layouts, and products
+    that read them."""
+    rows, cols = 36000, 60000
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device=DEV).normal_(generator=gen(1))
+    q = T.BlockTensor(rows, cols).quantize(x)
+    tail = x[-128 * 2 - 32:]          # whole blocks of rows from here: 35712 = 279 * 128
+    want, s = R.quantize(tail, 1, 128)
+    assert torch.equal(q.codes[-288:].view(R.E4M3).double(), want)
+    assert torch.equal(q.scales[:, -288:].double(), s.t())
+    want, s = R.quantize(tail, 128, 1)
+    assert torch.equal(q.codes_t[:, 35712:].view(R.E4M3).double(), want.t())
+    assert torch.equal(q.scales_t[-3:].double(), s)
+    w = T.BlockTensor(40, cols, shape=TILES).quantize(draw(gen(2), 40, cols, torch.bfloat16, 0.02))
+    c = torch.empty(rows, 40, dtype=torch.bfloat16, device=DEV)
+    T.block_gemm(q, w, c)
+    a = q.codes[-40:].view(R.E4M3).double() * R.spread(q.scales[:, -40:].double().t().contiguous(),
+                                                       1, 128, (40, cols))
+    b = as_values(w)
+    exact = torch.mm(a, b.t().contiguous())
+    R.assert_within(c[-40:], exact, R.product_bound(a, b, exact, torch.bfloat16), "rows past 2^31")
+    d = torch.empty(40, rows, dtype=torch.bfloat16, device=DEV)   # the same as the other operand
+    T.block_gemm(w, q, d)
+    R.assert_within(d[:, -40:], exact.t(), R.product_bound(b, a, exact.t(), torch.bfloat16), "columns past 2^31")
