@@ -236,7 +236,7 @@ hipError_t adamw_pass(const hq_adamw_tensor* t, int count, const hq_adamw_config
   a.host = host;
   a.device = device;
   int i = 0;
-  constexpr int64_t kMaxGrid = int64_t{1} << 30;
+  constexpr int64_t kMaxGrid = ((int64_t{1} << 32) - 1) / kThreads;   // a grid has less than 2^32 threads
   while (i < count) {
     // a table of tensors whose workgroups fit one grid
     a.count = 0;

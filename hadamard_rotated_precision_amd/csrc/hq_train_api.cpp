@@ -361,7 +361,7 @@ hq_status hq_adamw_step(const hq_adamw_tensor* tensors, int32_t count, const hq_
   if (!aligned(device_scalars, 4)) return HQ_ERR_ALIGN;
   for (int32_t i = 0; i < count; ++i) {
     const hq_adamw_tensor& t = tensors[i];
-    if (t.n < 0 || t.n > (int64_t{1} << 40)) return HQ_ERR_SHAPE;
+    if (t.n < 0 || t.n > (int64_t{1} << 34)) return HQ_ERR_SHAPE;
     if (!(t.weight_decay >= 0.0f && t.weight_decay <= 1e30f)) return HQ_ERR_MODE;
     if (t.n == 0) continue;
     if (!t.p || !t.grad || !t.m || !t.v) return HQ_ERR_NULL;

@@ -164,7 +164,7 @@ typedef struct {
   float *m_scales;   /* 8-bit states: ceil(n / 128) floats each; NULL for 32 bits */
   float *v_scales;
   void *copy;        /* NULL, or n elements of copy_dtype */
-  int64_t n;         /* 0 is skipped */
+  int64_t n;         /* at most 2^34; 0 is skipped */
   float weight_decay;
   int32_t reserved;  /* 0 */
 } hq_adamw_tensor;
@@ -193,7 +193,8 @@ hq_status hq_adamw_scalars_at(const hq_adamw_config *cfg, int64_t step, double g
 /* One step over `count` tensors (host array, read before the call returns). The step's scalars
  * are those in device memory when device_scalars is given (a captured step reads what it holds at
  * each replay; grad_scale may be written there by a kernel), else those of host_scalars.
- * p, m, v, copy and the scales of all tensors must not overlap each other. No workspace. */
+ * p, m, v, copy and the scales of all tensors must overlap neither each other nor a gradient.
+ * No workspace. */
 hq_status hq_adamw_step(const hq_adamw_tensor *tensors, int32_t count, const hq_adamw_config *cfg,
                         const hq_adamw_scalars *host_scalars,
                         const hq_adamw_scalars *device_scalars, void *stream);

@@ -219,7 +219,7 @@ def adamw_step(cfg=None, scalars=True, count=1, device=None, **kw):
     (dict(m=ODD, v=ODD), "HQ_ERR_DEVICE"),      # 8-bit codes
     (dict(cfg=adamw_cfg(state_bits=32), m=FAKE + 2), "HQ_ERR_ALIGN"),
     (dict(m_scales=FAKE + 2), "HQ_ERR_ALIGN"),
-    (dict(n=-1), "HQ_ERR_SHAPE"),
+    (dict(n=-1), "HQ_ERR_SHAPE"), (dict(n=2 ** 34 + 1), "HQ_ERR_SHAPE"), (dict(n=2 ** 34), "HQ_ERR_DEVICE"),
     (dict(weight_decay=-0.1), "HQ_ERR_MODE"), (dict(weight_decay=float("nan")), "HQ_ERR_MODE"),
     (dict(n=0, p=None, grad=None), "HQ_ERR_DEVICE"),    # an empty tensor needs no buffers
     (dict(cfg=adamw_cfg(state_bits=4)), "HQ_ERR_BITS"),
