@@ -292,28 +292,22 @@ class BlockTensor:
         return None if self.codes_t is None else self.codes_t[:, :self.rows]
 
 
-class _Workspace:
-    """Scratch of a layer's calls, and its size."""
-
-    def __init__(self, nbytes, device):
-        self.nbytes = nbytes
-        self.buf = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
-
-
 def block_gemm(a, b, c, a_side=B.HQ_SIDE_ROWS, b_side=B.HQ_SIDE_ROWS, accumulate=False, ws=None,
                stream=None):
     """hq_block_gemm: c (+)= a b^T over BlockTensors (HQ_SIDE_COLS reads the transposed codes).
-    ws: a uint8 tensor of hq_block_gemm_workspace_bytes, allocated here when missing."""
+    ws: a uint8 tensor of hq_block_gemm_workspace_bytes, allocated here when missing, from the
+    memory of the stream that uses it."""
     M, K = (a.rows, a.cols) if a_side == B.HQ_SIDE_ROWS else (a.cols, a.rows)
     N = b.rows if b_side == B.HQ_SIDE_ROWS else b.cols
     _check_matrix(c, M, N, "c", a.device)
     if b.device != a.device:
         raise ValueError("b is on %s, not on %s" % (b.device, a.device))
     if ws is None:
-        ws = torch.empty(max(B.hq_block_gemm_workspace_bytes(M, N, K), 16), dtype=torch.uint8,
-                         device=c.device)
-        if stream is not None:
-            ws.record_stream(stream)
+        with torch.cuda.stream(stream):
+            ws = torch.empty(max(B.hq_block_gemm_workspace_bytes(M, N, K), 16), dtype=torch.uint8,
+                             device=c.device)
+    elif ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != a.device:
+        raise ValueError("ws must be a contiguous uint8 tensor on %s" % a.device)
     B.check(_launch(B.hq_block_gemm, c, stream, a.st, a_side, b.st, b_side, c.data_ptr(),
                     HQ_DT[c.dtype], int(accumulate), ws.data_ptr(), ws.numel()), "hq_block_gemm")
 
@@ -379,7 +373,8 @@ class AdamW:
     steps_done: steps taken before.
 
     step(grads) takes the next step. Under HIP graph capture a step has to read its scalars from
-    device memory: step(grads, captured=True) launches with `device_scalars`, and
+    device memory: step(grads, captured=True) launches with `device_scalars` (a device tensor of
+    five 32-bit words: lr, step_size, inv_sqrt_bias2, grad_scale as floats, then the key), and
     advance(grad_scale) writes the next step's there before each replay."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01,
@@ -408,7 +403,8 @@ class AdamW:
         c.copy_dtype = HQ_DT[self.copies[0].dtype] if self.copies else c.param_dtype
         c.grad_dtype, c.state_bits, c.seed = c.param_dtype, state_bits, seed & 0xFFFFFFFF
         self._scalars = B.hq_adamw_scalars()
-        self._device_scalars = None
+        # made here: made under capture, it would be cleared again by each replay
+        self.device_scalars = torch.zeros(5, dtype=torch.float32, device=self.device)
         self._table = (B.hq_adamw_tensor * len(params))()
         self._rows = [(self._table[i], p.numel()) for i, p in enumerate(params)]
         for i, (t, p, s) in enumerate(zip(self._table, params, self.states)):
@@ -417,6 +413,18 @@ class AdamW:
             t.m, t.v = ptr(s["m"]), ptr(s["v"])
             t.m_scales, t.v_scales = ptr(s.get("m_scales")), ptr(s.get("v_scales"))
             t.copy = ptr(self.copies[i]) if self.copies else None
+        self._check_overlap()
+
+    def _check_overlap(self):
+        """All that a step writes has to be disjoint: a parameter listed twice would be updated by
+        two workgroups at once."""
+        keys = ("m", "v") + (("m_scales", "v_scales") if self.state_bits == 8 else ())
+        written = self.params + (self.copies or []) + [s[k] for s in self.states for k in keys]
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
+                       for t in written if t.numel())
+        for (_, end), (start, _) in zip(spans, spans[1:]):
+            if start < end:
+                raise ValueError("parameters, copies and states must not overlap")
 
     def _zeros(self, p):
         n, dev = p.numel(), p.device
@@ -450,14 +458,6 @@ class AdamW:
                     or t.device != self.device):
                 raise ValueError("state %s must be a contiguous %s tensor of %d elements on %s"
                                  % (k, dtype, size, self.device))
-
-    @property
-    def device_scalars(self):
-        """The device copy of the step's scalars that captured steps read (five 32-bit words: lr,
-        step_size, inv_sqrt_bias2, grad_scale as floats, then the key)."""
-        if self._device_scalars is None:
-            self._device_scalars = torch.zeros(5, dtype=torch.float32, device=self.device)
-        return self._device_scalars
 
     def set_lr(self, lr):
         self.cfg.lr = lr

@@ -373,3 +373,31 @@ def test_tensors_at_any_element(bits):
     assert torch.equal(flat["copy"], torch.cat(other.copies))
     for k in "mv":
         assert torch.equal(flat[k], torch.cat([s[k] for s in other.states]))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_capture_before_anything_else(bits):
+    """The first call of an optimizer may be the captured one: replays keep its scalars."""
+    p, grad = randn(gen(7), 700, 0.02), randn(gen(8), 700, 1e-3)
+    q = p.clone()
+    eager, taken = T.AdamW([p], state_bits=bits, **HYPER), T.AdamW([q], state_bits=bits, **HYPER)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        taken.step([grad], captured=True)
+    for _ in range(3):
+        eager.step([grad])
+        taken.advance()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(p, q)
+
+
+def test_overlapping_tensors_are_refused():
+    a, b = torch.zeros(100, device=DEV), torch.zeros(40, device=DEV)
+    whole = {"m": torch.zeros(140, device=DEV), "v": torch.zeros(100, device=DEV)}
+    for params, kw in (([a, b, a], {}), ([a, a[90:]], {}), ([a], dict(copies=[a])),
+                       ([a, b], dict(states=[{"m": whole["m"][:100], "v": whole["v"]},
+                                             {"m": whole["m"][99:139], "v": torch.zeros(40, device=DEV)}]))):
+        with pytest.raises(ValueError, match="overlap"):
+            T.AdamW(params, **kw)
+    T.AdamW([a[:50], a[50:], a[:0]])

@@ -585,3 +585,28 @@ def test_offsets_past_32_bits():
     d = torch.empty(40, rows, dtype=torch.bfloat16, device=DEV)   # the same as the other operand
     T.block_gemm(w, q, d)
     R.assert_within(d[:, -40:], exact.t(), R.product_bound(b, a, exact.t(), torch.bfloat16), "columns past 2^31")
+
+
+def test_workspace_of_another_stream(monkeypatch):
+    """The workspace that block_gemm makes comes from the memory of its stream: a block that the
+    current stream still works on is not handed out."""
+    a = T.BlockTensor(40, 4096).quantize(draw(gen(1), 40, 4096))
+    w = T.BlockTensor(300, 4096, shape=TILES).quantize(draw(gen(2), 300, 4096))
+    need = B.hq_block_gemm_workspace_bytes(40, 300, 4096)
+    assert need > 0
+    c = torch.empty(40, 300, device=DEV)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    used = []
+    call = B.hq_block_gemm
+    monkeypatch.setattr(B, "hq_block_gemm", lambda *x: (used.append(x[7]), call(*x))[1])
+    pending = torch.zeros(need, dtype=torch.uint8, device=DEV)
+    busy = pending.data_ptr()
+    del pending
+    T.block_gemm(a, w, c, stream=s)
+    torch.cuda.synchronize()
+    assert len(used) == 1 and used[0] != busy
+    for ws in (torch.empty(need, device=DEV), torch.empty(1, dtype=torch.uint8, device=DEV).expand(need),
+               torch.empty(need, dtype=torch.uint8)):
+        with pytest.raises(ValueError, match="ws"):
+            T.block_gemm(a, w, c, ws=ws)
