@@ -16,12 +16,14 @@
 // half the rate and the cost of widening the codes. Scales, their products and the sums over blocks
 // are fp32 throughout; the output is rounded once.
 //
-// What bounds it: power and the matrix pipe. At 8192 x 5120 x 13824 a launch takes 495 us
-// (2.34 PFLOP/s) at a shader clock of 1.83 GHz, the pipe busy two thirds of the time that a
-// workgroup is resident; 8192^3 runs at 2.5 PFLOP/s with fp32 scales and 2.8 with powers of two
+// What bounds it: power and the matrix pipe. At 8192 x 5120 x 13824 a launch takes 478 us
+// (2.43 PFLOP/s) at a shader clock of 1.83 GHz, the pipe busy two thirds of the time that a
+// workgroup is resident; 8192^3 runs at 2.6 PFLOP/s with fp32 scales and 2.8 with powers of two
 // (a library FP8 product without block scales: 2.9). A scale for each row of both operands (the
-// weight gradient) doubles the vector work to eight instructions per matrix instruction: 614 us,
-// 1.9 PFLOP/s, at 5120 x 13824 x 8192. fp32 outputs: 1.0 PFLOP/s at 4096^3.
+// weight gradient) doubles the vector work to eight instructions per matrix instruction: 582 us,
+// 2.0 PFLOP/s, at 5120 x 13824 x 8192. fp32 outputs: 1.0 PFLOP/s at 4096^3. From registers alone
+// the matrix pipe hides four vector instructions behind each of its own (33 of 32 cycles), and of
+// eight what does not wait for one another.
 // Tried and slower or equal: 32 x 32 x 64 instructions (8192^3, powers of two: 416 us against 400),
 // waves of 128 x 128 with accumulators in AGPRs (spills), fragments two rows ahead, double-buffered
 // fragments and four stages for the small tiles, a tail of half tiles for a partly filled last
@@ -66,6 +68,19 @@ enum ScaleMode { S_TILES = 0, S_ROWS = 1, S_POW2 = 2 };
 __device__ inline int lds_at(int row, int chunk) { return row * 128 + ((chunk ^ ((row >> 1) & 7)) << 4); }
 
 __device__ inline v8i join(v4i a, v4i b) { return v8i{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}; }
+
+// y[r] = f times x of lane k + r of each 16 (k a constant once loops are unrolled): the
+// multiplications read the other lane themselves, where the builtin's moves would be instructions
+// of their own. The two wait states are those between a vector write of x and such a read.
+__device__ __forceinline__ void times_lanes16(float x, int k, float f, float (&y)[4]) {
+  asm("s_nop 1\n\t"
+      "v_mul_f32_dpp %0, %4, %5 row_newbcast:%6 row_mask:0xf bank_mask:0xf\n\t"
+      "v_mul_f32_dpp %1, %4, %5 row_newbcast:%7 row_mask:0xf bank_mask:0xf\n\t"
+      "v_mul_f32_dpp %2, %4, %5 row_newbcast:%8 row_mask:0xf bank_mask:0xf\n\t"
+      "v_mul_f32_dpp %3, %4, %5 row_newbcast:%9 row_mask:0xf bank_mask:0xf"
+      : "=&v"(y[0]), "=&v"(y[1]), "=&v"(y[2]), "=&v"(y[3])
+      : "v"(x), "v"(f), "i"(k), "i"(k + 1), "i"(k + 2), "i"(k + 3));
+}
 
 // One dword per lane straight into LDS (lane l at lds + 4 l).
 __device__ inline void lds_dma4(__amdgpu_buffer_rsrc_t rs, float* lds, int voffset) {
@@ -188,23 +203,35 @@ __global__ __launch_bounds__(64 * NWP * NWQ * KS, 2) void block_gemm_kernel(Bloc
   v8h qh[TQ][EXACT ? 4 : 1], ph[TP][EXACT ? 4 : 1];   // EXACT: the codes' values as fp16
   float f[TQ], fn[TQ], spn = 0.0f;    // S_TILES: sp sq of this step and what the next needs; S_ROWS: sq
   int qe[TQ];                         // S_POW2: exponent bytes
-  v4f sp[TP];
+  // S_ROWS: lane 16 lg + x has p's scale of row 16 (4 h + x / 4) + 4 lg + x % 4 in sp[h], so the
+  // four of tile i that its 16 lanes need are those of lanes 4 (i % 4) + r in sp[i / 4]: two
+  // registers and small reads instead of four registers a tile and a 16-byte read each (the same
+  // product: 583 against 574 us)
+  constexpr int SH = (TP + 3) / 4;
+  float sp[SH], spr[SH];
   int pe[TP];
   auto read_p = [&](const int8_t* stg, int i) {
     pf[i] = frag(stg, wp * TP * 16 + i * 16 + lr);
-    if constexpr (MODE == S_ROWS) sp[i] = *reinterpret_cast<const v4f*>(p_scales(stg) + i * 16 + 4 * lg);
     if constexpr (MODE == S_POW2) pe[i] = __float_as_int(p_scales(stg)[i * 16 + lr]);
   };
   auto read_scales = [&](const int8_t* stg) {
 #pragma unroll
     for (int j = 0; j < TQ; ++j) fn[j] = q_scale(stg, j);
     if constexpr (MODE == S_TILES) spn = p_scales(stg)[0];
+    if constexpr (MODE == S_ROWS) {
+#pragma unroll
+      for (int h = 0; h < SH; ++h) spr[h] = p_scales(stg)[(4 * h + (lr >> 2)) % TP * 16 + 4 * lg + (lr & 3)];
+    }
   };
   auto halves = [&](const v8i& x, v8h (&h)[EXACT ? 4 : 1]) {
 #pragma unroll
     for (int e = 0; e < (EXACT ? 4 : 1); ++e) h[e] = f8_to_h8(x[2 * e], x[2 * e + 1]);
   };
   auto take_scales = [&]() {
+    if constexpr (MODE == S_ROWS) {
+#pragma unroll
+      for (int h = 0; h < SH; ++h) sp[h] = spr[h];
+    }
 #pragma unroll
     for (int j = 0; j < TQ; ++j) {
       if constexpr (MODE == S_POW2) qe[j] = __float_as_int(fn[j]) >> 23;
@@ -220,9 +247,15 @@ __global__ __launch_bounds__(64 * NWP * NWQ * KS, 2) void block_gemm_kernel(Bloc
     auto finish = [&](int n) {
       if constexpr (MODE != S_POW2) {
         const int i = slot_i(n), j = slot_j(n);
+        // the four products before the four fma's: each fma right behind its own product waits for
+        // it (5120 x 13824 x 8192: 602 against 583 us)
+        float s[4] = {f[j], f[j], f[j], f[j]};
+        if constexpr (MODE == S_ROWS) {
+          times_lanes16(sp[i / 4], 4 * (i % 4), f[j], s);
+          __builtin_amdgcn_sched_barrier(0);
+        }
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          acc[i][j][r] = __builtin_fmaf(u[n][r], MODE == S_TILES ? f[j] : sp[i][r] * f[j], acc[i][j][r]);
+        for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(u[n][r], s[r], acc[i][j][r]);
       }
     };
     const int ktn = k_first + (kt + 2) * KS + kg, k0 = ktn * 128;
@@ -257,10 +290,7 @@ __global__ __launch_bounds__(64 * NWP * NWQ * KS, 2) void block_gemm_kernel(Bloc
         constexpr int PER = (NDMA + N - FRONT - 1) / (N - FRONT);
 #pragma unroll
         for (int l = s * PER; l < (s + 1) * PER && l < NDMA; ++l) load_piece(ktn, cur, l, bp, bq);
-        // once row 0's last fma's, which use its scales, are past
-        constexpr int FREE = TQ - 1 + LAG > FRONT ? TQ - 1 + LAG - FRONT : 0;
-        static_assert(FREE < N - FRONT, "");
-        if (s == FREE) read_p(nxt, 0);
+        if (s == 0) read_p(nxt, 0);
         if (s == 1) read_scales(nxt);
         if ((s + 1) % HOLD == 0) qf[j] = q_frag(nxt, j);
       }
@@ -456,8 +486,18 @@ static hipError_t launch_mode(BlockGemmArgs a, hipStream_t st, int tok) {
     }
     case 128: return launch_tiled<Out, MODE, EXACT, 2, 2, 4, 4, 2, 1>(a, st, tok);
     default:
-      if constexpr (!EXACT)
-        return launch_tiled<Out, MODE, EXACT, 2, 4, 8, 4, MODE == S_POW2 ? 4 : 2, 1>(a, st, tok);
+      if constexpr (!EXACT) {
+        // rows held over the barrier: more of them lengthen the stretch in which the next loads are
+        // issued one by one, which costs less of the clock on long runs (8192 x 13824 x 5120: 470 us
+        // with three, 482 with two; 4096^3 back to back: 62.4 against 63.6); a single round of
+        // workgroups after other work waits for its loads instead (1000 tokens at 5120 x 13824 with
+        // their quantization: 71.4 against 69.0)
+        if constexpr (MODE == S_TILES) {
+          if (((a.M + 255) / 256) * ((a.N + 255) / 256) <= 256)
+            return launch_tiled<Out, MODE, EXACT, 2, 4, 8, 4, 2, 1>(a, st, tok);
+        }
+        return launch_tiled<Out, MODE, EXACT, 2, 4, 8, 4, MODE == S_POW2 ? 4 : 3, 1>(a, st, tok);
+      }
   }
   return hipErrorInvalidValue;
 }
