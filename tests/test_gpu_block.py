@@ -610,3 +610,21 @@ def test_workspace_of_another_stream(monkeypatch):
                torch.empty(need, dtype=torch.uint8)):
         with pytest.raises(ValueError, match="ws"):
             T.block_gemm(a, w, c, ws=ws)
+
+
+@pytest.mark.parametrize("M,N,K", [(4500, 8300, 700), (8200, 4400, 1030), (5120, 13824, 384)])
+def test_gemm_outputs_of_many_rounds(M, N, K):
+    """More large tiles than compute units, odd and even numbers of K blocks: sampled rows of it."""
+    rows = torch.cat([torch.arange(0, M, 251), torch.arange(M - 9, M)]).to(DEV)
+    for k, (dtype, kinds, shapes) in enumerate([
+            (torch.bfloat16, (F32, F32), (ROWS, TILES)), (torch.float16, (F32, F32), (ROWS, ROWS)),
+            (torch.bfloat16, (F32, POW2), (TILES, ROWS)), (torch.bfloat16, (POW2, POW2), (ROWS, TILES)),
+            (torch.float32, (F32, F32), (ROWS, ROWS))]):
+        print("[case] gemm", M, N, K, dtype, kinds, shapes, flush=True)
+        a, b = operands(M, N, K, kinds, shapes, k)
+        c = torch.full((M, N), float("nan"), dtype=dtype, device=DEV)
+        T.block_gemm(a, b, c)
+        assert not c.isnan().any()
+        va, vb = as_values(a)[rows].contiguous(), as_values(b)
+        want = torch.mm(va, vb.t().contiguous())
+        R.assert_within(c[rows], want, R.product_bound(va, vb, want, dtype), "sampled rows")
