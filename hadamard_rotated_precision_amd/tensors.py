@@ -368,7 +368,8 @@ class AdamW:
 
     state_bits: 32 (fp32 states) or 8 (E4M3 codes with a scale for each 128 elements).
     weight_decay: one number, or one for each tensor. copies: tensors of one dtype that receive
-    the updated parameters (the low-precision weights of the next forward). states: dicts of m, v
+    the updated parameters (the low-precision weights of the next forward); a copy may be its own
+    parameter, which then is written once. states: dicts of m, v
     (and m_scales, v_scales for 8 bits) to go on from, used in place; zeros without it.
     steps_done: steps taken before.
 
@@ -412,14 +413,20 @@ class AdamW:
             t.p, t.n, t.weight_decay = ptr(p), p.numel(), decay[i]
             t.m, t.v = ptr(s["m"]), ptr(s["v"])
             t.m_scales, t.v_scales = ptr(s.get("m_scales")), ptr(s.get("v_scales"))
-            t.copy = ptr(self.copies[i]) if self.copies else None
+            copy = self.copies[i] if self.copies else None
+            t.copy = None if copy is None or self._is_same(copy, p) else ptr(copy)
         self._check_overlap()
 
+    @staticmethod
+    def _is_same(copy, p):
+        return copy.dtype == p.dtype and copy.data_ptr() == p.data_ptr()
+
     def _check_overlap(self):
-        """All that a step writes has to be disjoint: a parameter listed twice would be updated by
-        two workgroups at once."""
+        """All that a step writes has to be disjoint (a copy that is its own parameter aside): a
+        parameter listed twice would be updated by two workgroups at once."""
         keys = ("m", "v") + (("m_scales", "v_scales") if self.state_bits == 8 else ())
-        written = self.params + (self.copies or []) + [s[k] for s in self.states for k in keys]
+        written = self.params + [s[k] for s in self.states for k in keys]
+        written += [c for c, p in zip(self.copies or [], self.params) if not self._is_same(c, p)]
         spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
                        for t in written if t.numel())
         for (_, end), (start, _) in zip(spans, spans[1:]):

@@ -193,7 +193,8 @@ hq_status hq_adamw_scalars_at(const hq_adamw_config *cfg, int64_t step, double g
 /* One step over `count` tensors (host array, read before the call returns). The step's scalars
  * are those in device memory when device_scalars is given (a captured step reads what it holds at
  * each replay; grad_scale may be written there by a kernel), else those of host_scalars.
- * p, m, v, copy and the scales of all tensors must overlap neither each other nor a gradient.
+ * p, m, v, copy and the scales of all tensors must overlap neither each other nor a gradient; a
+ * copy of the parameters' type may be its own p.
  * No workspace. */
 hq_status hq_adamw_step(const hq_adamw_tensor *tensors, int32_t count, const hq_adamw_config *cfg,
                         const hq_adamw_scalars *host_scalars,

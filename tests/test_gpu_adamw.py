@@ -393,11 +393,26 @@ def test_capture_before_anything_else(bits):
 
 
 def test_overlapping_tensors_are_refused():
-    a, b = torch.zeros(100, device=DEV), torch.zeros(40, device=DEV)
+    a, b, c = torch.zeros(100, device=DEV), torch.zeros(40, device=DEV), torch.zeros(100, device=DEV)
     whole = {"m": torch.zeros(140, device=DEV), "v": torch.zeros(100, device=DEV)}
-    for params, kw in (([a, b, a], {}), ([a, a[90:]], {}), ([a], dict(copies=[a])),
+    for params, kw in (([a, b, a], {}), ([a, a[90:]], {}), ([a, c], dict(copies=[c, a])),
                        ([a, b], dict(states=[{"m": whole["m"][:100], "v": whole["v"]},
                                              {"m": whole["m"][99:139], "v": torch.zeros(40, device=DEV)}]))):
         with pytest.raises(ValueError, match="overlap"):
             T.AdamW(params, **kw)
     T.AdamW([a[:50], a[50:], a[:0]])
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_copy_may_be_its_own_parameter(bits):
+    """bf16 parameters whose bf16 copies are themselves: the bits of a step without copies."""
+    start = [randn(gen(k), n, 0.02).bfloat16() for k, n in enumerate((1, 300, 4097))]
+    grads = [randn(gen(9), p.numel(), 1e-3) for p in start]
+    alone, same = [p.clone() for p in start], [p.clone() for p in start]
+    a = T.AdamW(alone, state_bits=bits, **HYPER)
+    b = T.AdamW(same, state_bits=bits, copies=[p.to(torch.bfloat16) for p in same], **HYPER)
+    for _ in range(3):
+        a.step(grads)
+        b.step(grads)
+    for x, y, z in zip(alone, same, start):
+        assert torch.equal(x, y) and not torch.equal(x, z)
