@@ -2,8 +2,8 @@
 //
 // The formulas stand in include/hq_train.h. What bounds it: bytes; per element the parameter and
 // the states are read and written once and the gradient is read once. 88 M elements with fp32
-// parameters, bf16 gradients and a bf16 copy: 457 us with 32-bit states (5.4 TB/s), 261 with 8-bit
-// ones (5.5 TB/s; 304 before one square root and a three-operation reciprocal took the place of two
+// parameters, bf16 gradients and a bf16 copy: 457 us with 32-bit states (5.4 TB/s), 265 with 8-bit
+// ones (5.4 TB/s; 304 before one square root and a three-operation reciprocal took the place of two
 // and a division: the vector work of 8-bit states is close behind the bytes). Stores past the
 // caches changed nothing.
 //
