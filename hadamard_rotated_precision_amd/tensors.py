@@ -1,6 +1,9 @@
 """Device-memory plumbing around the C ABI: torch allocates the buffers (codes, scales,
 outputs, workspace) and names the stream; the binding passes raw pointers to libhq.
 No arithmetic of the method happens here."""
+import itertools
+import operator
+
 import numpy as np
 import torch
 
@@ -184,7 +187,7 @@ def _launch(fn, t, stream, *args):
     given stream or the device's current one."""
     dev = t.device.index
     raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-    if dev == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():
         return fn(*args, raw)
     with torch.cuda.device(dev):
         return fn(*args, raw)
@@ -373,6 +376,10 @@ class AdamW:
     (and m_scales, v_scales for 8 bits) to go on from, used in place; zeros without it.
     steps_done: steps taken before.
 
+    Parameters, copies and states may be bound anew (p.data = ..., opt.states[i]["m"] = ...): the
+    next step checks them again and works on the new memory. A captured step keeps the addresses of
+    its capture.
+
     step(grads) takes the next step. Under HIP graph capture a step has to read its scalars from
     device memory: step(grads, captured=True) launches with `device_scalars` (a device tensor of
     five 32-bit words: lr, step_size, inv_sqrt_bias2, grad_scale as floats, then the key), and
@@ -390,32 +397,63 @@ class AdamW:
         if state_bits not in (8, 32):
             raise ValueError("state_bits is 8 or 32")
         self.params, self.device, self.step_count = params, params[0].device, int(steps_done)
-        self.state_bits = state_bits
-        self._check("parameter", params, params[0].dtype)
+        self.state_bits, self._dtype = state_bits, params[0].dtype
+        self._check("parameter", params, self._dtype)
         self.copies = None if copies is None else list(copies)
-        if self.copies is not None:
-            self._check("copy", self.copies, self.copies[0].dtype if self.copies else None)
+        self._copy_dtype = self.copies[0].dtype if self.copies else self._dtype
         self.states = [self._zeros(p) for p in params] if states is None else list(states)
         if len(self.states) != len(params):
             raise ValueError("one state for each parameter is needed")
         c = self.cfg = B.hq_adamw_config()
         c.lr, (c.beta1, c.beta2), c.eps = lr, betas, eps
-        c.param_dtype = HQ_DT[params[0].dtype]
-        c.copy_dtype = HQ_DT[self.copies[0].dtype] if self.copies else c.param_dtype
+        self._state_keys = ("m", "v") + (("m_scales", "v_scales") if state_bits == 8 else ())
+        self._state_of = operator.itemgetter(*self._state_keys)
+        self._table, self._decay = (B.hq_adamw_tensor * len(params))(), decay
+        self._bind()
+        c.param_dtype, c.copy_dtype = HQ_DT[self._dtype], HQ_DT[self._copy_dtype]
         c.grad_dtype, c.state_bits, c.seed = c.param_dtype, state_bits, seed & 0xFFFFFFFF
         self._scalars = B.hq_adamw_scalars()
         # made here: made under capture, it would be cleared again by each replay
         self.device_scalars = torch.zeros(5, dtype=torch.float32, device=self.device)
-        self._table = (B.hq_adamw_tensor * len(params))()
-        self._rows = [(self._table[i], p.numel()) for i, p in enumerate(params)]
-        for i, (t, p, s) in enumerate(zip(self._table, params, self.states)):
+
+    def _addresses(self):
+        """Those of every tensor that a step writes."""
+        states = itertools.chain.from_iterable(map(self._state_of, self.states))
+        return list(map(torch.Tensor.data_ptr,
+                        itertools.chain(self.params, self.copies or (), states)))
+
+    def _bind(self):
+        """Check the tensors that a step works on and note their addresses."""
+        if len(self.params) != len(self._table) or len(self.states) != len(self._table):
+            raise ValueError("%d parameters and %d states for an optimizer of %d"
+                             % (len(self.params), len(self.states), len(self._table)))
+        self._check("parameter", self.params, self._dtype)
+        if self.copies is not None:
+            self._check("copy", self.copies, self._copy_dtype)
+        for p, s in zip(self.params, self.states):
             self._check_state(s, p.numel())
-            t.p, t.n, t.weight_decay = ptr(p), p.numel(), decay[i]
+        self._check_overlap()
+        rows = []
+        for i, (t, p, s) in enumerate(zip(self._table, self.params, self.states)):
+            t.p, t.n, t.weight_decay = ptr(p), p.numel(), self._decay[i]
             t.m, t.v = ptr(s["m"]), ptr(s["v"])
-            t.m_scales, t.v_scales = ptr(s.get("m_scales")), ptr(s.get("v_scales"))
+            t.m_scales, t.v_scales = (ptr(s[k]) if self.state_bits == 8 else None
+                                      for k in ("m_scales", "v_scales"))
             copy = self.copies[i] if self.copies else None
             t.copy = None if copy is None or self._is_same(copy, p) else ptr(copy)
-        self._check_overlap()
+            rows.append((t, p.numel()))
+        self._rows = rows
+        self._bound = self._addresses()
+
+    def _is_bound(self):
+        """The table's addresses are the tensors', whose elements are still in order. (A call for
+        each tensor: 2 us on the host for 12 parameters with 32-bit states.)"""
+        try:
+            return (self._addresses() == self._bound
+                    and all(map(torch.Tensor.is_contiguous,
+                                itertools.chain(self.params, self.copies or ()))))
+        except KeyError:    # a state's entry is gone
+            return False
 
     @staticmethod
     def _is_same(copy, p):
@@ -424,8 +462,7 @@ class AdamW:
     def _check_overlap(self):
         """All that a step writes has to be disjoint (a copy that is its own parameter aside): a
         parameter listed twice would be updated by two workgroups at once."""
-        keys = ("m", "v") + (("m_scales", "v_scales") if self.state_bits == 8 else ())
-        written = self.params + [s[k] for s in self.states for k in keys]
+        written = self.params + [s[k] for s in self.states for k in self._state_keys]
         written += [c for c, p in zip(self.copies or [], self.params) if not self._is_same(c, p)]
         spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
                        for t in written if t.numel())
@@ -482,13 +519,15 @@ class AdamW:
         """One step with one gradient for each parameter (one dtype for all)."""
         if len(grads) != len(self.params):
             raise ValueError("%d gradients for %d parameters" % (len(grads), len(self.params)))
-        dtype, device = grads[0].dtype, self.device
+        dtype, index = grads[0].dtype, self.params[0].get_device()
         if dtype not in HQ_DT:
             raise ValueError("gradients have dtype %s: fp32, fp16 or bf16 is needed" % dtype)
+        if not self._is_bound():
+            self._bind()
         for g, (row, n) in zip(grads, self._rows):
-            if g.dtype != dtype or g.numel() != n or g.device != device or not g.is_contiguous():
+            if g.dtype != dtype or g.numel() != n or g.get_device() != index or not g.is_contiguous():
                 raise ValueError("gradients must be contiguous %s tensors on %s with their "
-                                 "parameters' numbers of elements" % (dtype, device))
+                                 "parameters' numbers of elements" % (dtype, self.device))
             row.grad = g.data_ptr()
         self.cfg.grad_dtype = HQ_DT[dtype]
         if captured:

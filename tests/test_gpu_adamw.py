@@ -416,3 +416,30 @@ def test_a_copy_may_be_its_own_parameter(bits):
         b.step(grads)
     for x, y, z in zip(alone, same, start):
         assert torch.equal(x, y) and not torch.equal(x, z)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_rebound_tensors_give_the_bits_of_an_optimizer_made_anew(bits):
+    """After p.data = ..., a state loaded by assignment and a new copy, steps go on from there and
+    leave the old memory as it was."""
+    n = 1003
+    g = gen(21)
+    p, grads = randn(g, n, 0.02), [randn(g, n, 1e-3) for _ in range(3)]
+    copy = p.bfloat16()
+    opt = T.AdamW([p], state_bits=bits, copies=[copy], seed=2, **HYPER)
+    opt.step([grads[0]])
+    q = T.AdamW([p.clone()], state_bits=bits, copies=[copy.clone()], seed=2, steps_done=1,
+                states=[{k: t.clone() for k, t in opt.states[0].items()}], **HYPER)
+    old = [p.data, copy.data] + list(opt.states[0].values())
+    kept = [t.clone() for t in old]
+    p.data, copy.data = p.data.clone(), copy.data.clone()
+    for k in list(opt.states[0]):
+        opt.states[0][k] = opt.states[0][k].clone()
+    for grad in grads[1:]:
+        opt.step([grad])
+        q.step([grad])
+    assert torch.equal(p, q.params[0]) and torch.equal(copy, q.copies[0])
+    for k in opt.states[0]:
+        assert torch.equal(opt.states[0][k], q.states[0][k]), k
+    for was, now in zip(kept, old):
+        assert torch.equal(was, now)

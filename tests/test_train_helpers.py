@@ -1,0 +1,114 @@
+"""The torch helpers of include/hq_train.h on the CPU: what they hand to the library (the launch is
+replaced by a stand-in that looks at the arguments), and what they refuse before it."""
+import pytest
+import torch
+
+from hadamard_rotated_precision_amd import binding as B
+from hadamard_rotated_precision_amd import tensors as T
+
+
+@pytest.fixture
+def launches(monkeypatch):
+    """Argument lists of the calls that would have reached the library."""
+    calls = []
+    monkeypatch.setattr(T, "_launch", lambda fn, t, stream, *args: calls.append(args) or B.HQ_OK)
+    return calls
+
+
+FIELDS = {32: ("m", "v"), 8: ("m", "v", "m_scales", "v_scales")}
+
+
+def adamw(bits, copies=False):
+    params = [torch.zeros(n) for n in (300, 7)]
+    kw = dict(copies=[p.bfloat16() for p in params]) if copies else {}
+    return T.AdamW(params, state_bits=bits, **kw), [torch.zeros(n) for n in (300, 7)]
+
+
+def table_is_current(call, opt):
+    table = call[0]
+    for i, (p, s) in enumerate(zip(opt.params, opt.states)):
+        assert table[i].p == p.data_ptr()
+        for k in FIELDS[opt.state_bits]:
+            assert getattr(table[i], k) == s[k].data_ptr(), k
+        assert table[i].copy == (opt.copies[i].data_ptr() if opt.copies else None)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_follows_tensors_that_are_rebound(bits, launches):
+    """p.data = ..., a state's entry, an entry of the lists: the step works on the new memory."""
+    opt, grads = adamw(bits, copies=True)
+    opt.step(grads)
+    opt.params[0].data = torch.ones(300)
+    opt.step(grads)
+    for k in FIELDS[bits]:
+        opt.states[1][k] = opt.states[1][k].clone()
+    opt.step(grads)
+    opt.copies[1].data = opt.copies[1].data.clone()
+    opt.step(grads)
+    opt.params[1] = torch.ones(7)
+    opt.step(grads)
+    opt.copies[1] = torch.ones(7, dtype=torch.bfloat16)
+    opt.step(grads)
+    assert len(launches) == 6 and opt.step_count == 6
+    for call in launches[-1:]:
+        table_is_current(call, opt)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("what", range(5))
+def test_adamw_follows_each_rebinding_at_once(bits, what, launches):
+    opt, grads = adamw(bits, copies=True)
+    opt.step(grads)
+    if what == 0:
+        opt.params[0].data = torch.ones(300)
+    elif what == 1:
+        opt.states[0]["m"] = opt.states[0]["m"].clone()
+    elif what == 2:
+        opt.states[1]["v"].data = opt.states[1]["v"].clone()
+    elif what == 3:
+        opt.copies[0].data = opt.copies[0].clone()
+    else:
+        opt.states[0] = {k: t.clone() for k, t in opt.states[0].items()}
+    opt.step(grads)
+    table_is_current(launches[-1], opt)
+
+
+def test_adamw_checks_what_is_rebound(launches):
+    """The checks of the constructor hold for a tensor that takes another's place."""
+    def broken(change, match):
+        opt, grads = adamw(8, copies=True)
+        change(opt)
+        with pytest.raises(ValueError, match=match):
+            opt.step(grads)
+        with pytest.raises(ValueError, match=match):    # and again: it stays refused
+            opt.step(grads)
+        assert not launches and opt.step_count == 0
+
+    def set_data(t, new):
+        t.data = new
+
+    broken(lambda o: set_data(o.params[0], torch.zeros(300).half()), "dtype")
+    broken(lambda o: set_data(o.params[0], torch.zeros(299)), "300|299")
+    broken(lambda o: set_data(o.params[0], torch.zeros(300, 2)[:, 0]), "contiguous")
+    broken(lambda o: set_data(o.copies[1], torch.zeros(7)), "dtype")
+    broken(lambda o: set_data(o.params[1], o.params[0].data[10:17]), "overlap")
+    broken(lambda o: o.states[0].update(m=o.states[0]["v"]), "overlap")
+    broken(lambda o: o.states[0].update(m=torch.zeros(300)), "state m")
+    broken(lambda o: o.states[1].update(v_scales=torch.zeros(2)), "state v_scales")
+    broken(lambda o: o.states[1].pop("m_scales"), "m_scales")
+    broken(lambda o: o.params.append(torch.zeros(3)), "param")
+
+
+@pytest.mark.parametrize("copy", [False, True])
+def test_adamw_refuses_a_transposed_tensor_at_the_same_address(copy, launches):
+    """p.data = p.data.t() keeps the address and changes the order of the elements."""
+    p, c = torch.zeros(6, 5), torch.zeros(6, 5).half()
+    opt = T.AdamW([p], copies=[c])
+    opt.step([torch.zeros(6, 5)])
+    if copy:
+        c.data = c.data.t()
+    else:
+        p.data = p.data.t()
+    with pytest.raises(ValueError, match="contiguous"):
+        opt.step([torch.zeros(5, 6)])
+    assert len(launches) == 1
