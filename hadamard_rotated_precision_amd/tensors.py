@@ -184,7 +184,10 @@ def _blocks(n):
 
 def _launch(fn, t, stream, *args):
     """fn(*args, stream) with t's device current (a call launches on the current device), on the
-    given stream or the device's current one."""
+    given stream or the device's current one. The callers check that their other tensors are where
+    t is; host memory is refused here, for a kernel would fault on it."""
+    if not t.is_cuda:
+        raise ValueError("tensors on a GPU are needed, not on %s" % t.device)
     dev = t.device.index
     raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
     if dev == torch._C._cuda_getDevice():

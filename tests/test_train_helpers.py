@@ -112,3 +112,30 @@ def test_adamw_refuses_a_transposed_tensor_at_the_same_address(copy, launches):
     with pytest.raises(ValueError, match="contiguous"):
         opt.step([torch.zeros(5, 6)])
     assert len(launches) == 1
+
+
+class AnyStream:
+    cuda_stream = 0
+
+
+def test_host_memory_never_reaches_a_call(monkeypatch):
+    """Tensors in host memory agree with one another about their device; the library would launch
+    on their addresses all the same."""
+    reached = []
+    for name in ("hq_block_quantize", "hq_block_gemm", "hq_block_linear_fwd",
+                 "hq_block_linear_bwd_input", "hq_block_linear_bwd_weight", "hq_adamw_step"):
+        monkeypatch.setattr(B, name, lambda *a: reached.append(a) or B.HQ_OK)
+    x, y, w = torch.zeros(4, 64), torch.zeros(4, 32), torch.zeros(32, 64)
+    a, b = T.BlockTensor(4, 64, device="cpu"), T.BlockTensor(32, 64, shape=B.HQ_BLOCK_TILES, device="cpu")
+    layer = T.BlockLayer(4, 64, 32, weight=b)
+    opt = T.AdamW([torch.zeros(5)])
+    ws = torch.zeros(1 << 20, dtype=torch.uint8)
+    for call in (lambda s: a.quantize(x, stream=s), lambda s: layer.set_weight(w, s),
+                 lambda s: layer.fwd(x, y, s), lambda s: layer.bwd_input(y, x, s),
+                 lambda s: layer.bwd_weight(w, stream=s),
+                 lambda s: T.block_gemm(a, b, y, ws=ws, stream=s),
+                 lambda s: opt.step([torch.zeros(5)], stream=s)):
+        for stream in (AnyStream(), None):
+            with pytest.raises(ValueError, match="GPU"):
+                call(stream)
+    assert not reached and opt.step_count == 0
