@@ -1,3 +1,4 @@
+import inspect
 import os
 import sys
 
@@ -12,6 +13,16 @@ def pytest_configure(config):
     config.addinivalue_line("markers", "gpu: needs an MI355X (gfx950) GPU")
 
 
+def stops_at_the_device_check(item):
+    """The test expects HQ_ERR_DEVICE (a parameter of this case, or named in the test's body): it
+    hands over fake addresses that pass every other check, and would launch on them on a GPU."""
+    expected = getattr(item, "callspec", None)
+    if expected is not None and "HQ_ERR_DEVICE" in [v for v in expected.params.values() if isinstance(v, str)]:
+        return True
+    source = inspect.getsource(item.function)
+    return "HQ_ERR_DEVICE" in source[source.index("def "):]    # without the list of cases
+
+
 def pytest_collection_modifyitems(config, items):
     # GPU tests skip cleanly when no GPU is visible; on a machine with one they run.
     try:
@@ -20,6 +31,10 @@ def pytest_collection_modifyitems(config, items):
     except Exception:  # pragma: no cover
         have_gpu = False
     if have_gpu:
+        skip = pytest.mark.skip(reason="only safe without a GPU: its fake addresses pass the checks")
+        for item in items:
+            if "gpu" not in item.keywords and stops_at_the_device_check(item):
+                item.add_marker(skip)
         return
     skip = pytest.mark.skip(reason="no GPU visible")
     for item in items:
