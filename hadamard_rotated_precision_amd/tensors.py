@@ -386,7 +386,8 @@ class AdamW:
     step(grads) takes the next step. Under HIP graph capture a step has to read its scalars from
     device memory: step(grads, captured=True) launches with `device_scalars` (a device tensor of
     five 32-bit words: lr, step_size, inv_sqrt_bias2, grad_scale as floats, then the key), and
-    advance(grad_scale) writes the next step's there before each replay."""
+    advance(grad_scale, stream) writes the next step's there before each replay, on the stream of
+    the replay."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01,
                  state_bits=32, copies=None, states=None, seed=0, steps_done=0):
@@ -509,14 +510,19 @@ class AdamW:
     def set_lr(self, lr):
         self.cfg.lr = lr
 
-    def advance(self, grad_scale=1.0):
-        """Count one step and write its scalars to device_scalars (in stream order)."""
+    def advance(self, grad_scale=1.0, stream=None):
+        """Count one step and write its scalars to device_scalars, in the order of the given stream
+        (or the current one), without waiting for it. Each call's words go through pinned memory of
+        their own, which torch hands out again once their copy is done."""
+        if stream is not None and stream.device != self.device:
+            raise ValueError("the stream is of %s, not of %s" % (stream.device, self.device))
         s = self._scalars
         B.check(B.hq_adamw_scalars_at(self.cfg, self.step_count + 1, grad_scale, s),
                 "hq_adamw_scalars_at")
         self.step_count += 1
-        host = torch.frombuffer(bytearray(bytes(s)), dtype=torch.float32)
-        self.device_scalars.copy_(host)
+        host = torch.frombuffer(bytearray(bytes(s)), dtype=torch.float32).pin_memory()
+        with torch.cuda.stream(stream):
+            self.device_scalars.copy_(host, non_blocking=True)
 
     def step(self, grads, grad_scale=1.0, captured=False, stream=None):
         """One step with one gradient for each parameter (one dtype for all)."""

@@ -443,3 +443,51 @@ def test_rebound_tensors_give_the_bits_of_an_optimizer_made_anew(bits):
         assert torch.equal(opt.states[0][k], q.states[0][k]), k
     for was, now in zip(kept, old):
         assert torch.equal(was, now)
+
+
+def busy(stream=None):
+    """Tens of milliseconds of work on a stream, and the event behind it."""
+    a = torch.ones(8192, 8192, dtype=torch.bfloat16, device=DEV)
+    torch.cuda.synchronize()
+    done = torch.cuda.Event()
+    with torch.cuda.stream(stream):
+        for _ in range(60):
+            torch.mm(a, a)
+        done.record()
+    return done
+
+
+def test_advance_does_not_wait_for_the_stream():
+    opt = T.AdamW([torch.zeros(100, device=DEV)], **HYPER)
+    opt.advance()       # the first call allocates
+    done = busy()
+    opt.advance()
+    assert not done.query(), "the host waited for the work before it"
+    torch.cuda.synchronize()
+    assert done.query()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_captured_steps_run_ahead_on_a_stream_of_their_own(bits):
+    """Many steps handed over at once, with the scalars of each in the order of the stream."""
+    p, grad = randn(gen(7), 3000, 0.02), randn(gen(8), 3000, 1e-3)
+    q = p.clone()
+    eager, taken = T.AdamW([p], state_bits=bits, **HYPER), T.AdamW([q], state_bits=bits, **HYPER)
+    s = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        taken.step([grad], captured=True)
+    torch.cuda.synchronize()
+    for k in range(50):
+        eager.step([grad], grad_scale=1.0 + k)
+    torch.cuda.synchronize()
+    done = busy(s)
+    for k in range(50):
+        taken.advance(grad_scale=1.0 + k, stream=s)
+        with torch.cuda.stream(s):
+            graph.replay()
+    assert not done.query()
+    torch.cuda.synchronize()
+    assert torch.equal(p, q)
+    for name in eager.states[0]:
+        assert torch.equal(eager.states[0][name], taken.states[0][name])
