@@ -525,7 +525,10 @@ class AdamW:
             self.device_scalars.copy_(host, non_blocking=True)
 
     def step(self, grads, grad_scale=1.0, captured=False, stream=None):
-        """One step with one gradient for each parameter (one dtype for all)."""
+        """One step with one gradient for each parameter (one dtype for all). A captured one takes
+        its gradient scale from advance()."""
+        if captured and grad_scale != 1.0:
+            raise ValueError("a captured step reads its gradient scale from what advance() wrote")
         if len(grads) != len(self.params):
             raise ValueError("%d gradients for %d parameters" % (len(grads), len(self.params)))
         dtype, index = grads[0].dtype, self.params[0].get_device()

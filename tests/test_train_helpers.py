@@ -139,3 +139,13 @@ def test_host_memory_never_reaches_a_call(monkeypatch):
             with pytest.raises(ValueError, match="GPU"):
                 call(stream)
     assert not reached and opt.step_count == 0
+
+
+def test_captured_step_takes_no_gradient_scale(launches):
+    """A captured step reads its scale from device_scalars: one given to it would be lost."""
+    opt, grads = adamw(32)
+    with pytest.raises(ValueError, match="advance"):
+        opt.step(grads, grad_scale=0.5, captured=True)
+    assert not launches
+    opt.step(grads, captured=True)
+    assert len(launches) == 1 and opt.step_count == 0
