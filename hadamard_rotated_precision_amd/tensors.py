@@ -212,7 +212,13 @@ class BlockTensor:
     """Caller-owned storage of a block-scaled FP8 matrix (hq_block_tensor): E4M3 codes
     (rows x pitch), transposed codes (cols x pitch) and their scales. ROWS blocks (1 x 128) have
     scales (column blocks x rows) and scales_t (row blocks x cols); TILES (128 x 128) have one
-    scales (row blocks x column blocks) for both layouts."""
+    scales (row blocks x column blocks) for both layouts. New values go into the buffers; the
+    buffers themselves stay, for the library's struct holds their addresses."""
+
+    codes = property(operator.attrgetter("_codes"))
+    codes_t = property(operator.attrgetter("_codes_t"))
+    scales = property(operator.attrgetter("_scales"))
+    scales_t = property(operator.attrgetter("_scales_t"))
 
     def __init__(self, rows, cols, shape=B.HQ_BLOCK_ROWS, scale=B.HQ_BSCALE_F32, codes=True,
                  codes_t=True, device="cuda"):
@@ -232,7 +238,7 @@ class BlockTensor:
 
     def _set(self, rows, cols, shape, scale, codes, codes_t, scales, scales_t):
         self.rows, self.cols, self.shape, self.scale = rows, cols, shape, scale
-        self.codes, self.codes_t, self.scales, self.scales_t = codes, codes_t, scales, scales_t
+        self._codes, self._codes_t, self._scales, self._scales_t = codes, codes_t, scales, scales_t
         self.device = next(t for t in (codes, codes_t, scales) if t is not None).device
         st = self.st = B.hq_block_tensor()
         st.codes, st.codes_t = ptr(codes), ptr(codes_t)

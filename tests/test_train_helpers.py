@@ -149,3 +149,15 @@ def test_captured_step_takes_no_gradient_scale(launches):
     assert not launches
     opt.step(grads, captured=True)
     assert len(launches) == 1 and opt.step_count == 0
+
+
+@pytest.mark.parametrize("name", ["codes", "codes_t", "scales", "scales_t"])
+def test_block_tensor_keeps_its_buffers(name):
+    """The library's struct holds the buffers' addresses: another tensor in their place would leave
+    it with those of freed memory."""
+    for q in (T.BlockTensor(40, 300, device="cpu"),
+              T.BlockTensor.wrap(torch.zeros(40, 304, dtype=torch.uint8), torch.zeros(1, 3), 40, 300)):
+        old = getattr(q, name)
+        with pytest.raises(AttributeError):
+            setattr(q, name, torch.zeros(3))
+        assert getattr(q, name) is old
