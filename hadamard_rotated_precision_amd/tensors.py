@@ -257,7 +257,7 @@ class BlockTensor:
         """A matrix whose codes exist already (weights of a checkpoint): codes (rows x pitch, the
         bytes from cols to the next multiple of 16 zero), scales as above. The buffers are used
         as they are. Checks their shapes and, once, on the host, that scales of kind POW2 are
-        powers of two."""
+        powers of two from 2^-126 up, NaN, or 0 over codes that are zero."""
         self = cls.__new__(cls)
         parts = [("codes", codes, rows, cols, torch.uint8),
                  ("codes_t", codes_t, cols, rows, torch.uint8)]
@@ -281,13 +281,31 @@ class BlockTensor:
                 end = t.storage_offset() + (r - 1) * cls._pitch(t) + pitch16(c)
                 if end > t.untyped_storage().nbytes():
                     raise ValueError("%s: the last row must reach to the next multiple of 16 bytes" % name)
-        for t in (scales, scales_t):
-            if scale == B.HQ_BSCALE_POW2 and t is not None and t.numel():
-                mantissa, _ = torch.frexp(t)
-                if not bool(((mantissa == 0.5) | (t == 0) | t.isnan()).all()):
-                    raise ValueError("scales of kind POW2 must be powers of two")
+        if scale == B.HQ_BSCALE_POW2:
+            # by row of codes and block of columns, for each layout
+            if shape == B.HQ_BLOCK_TILES:
+                every = scales[:, :_blocks(cols)]
+                cls._check_pow2(every, codes, 128, cols)
+                if codes_t is not None:
+                    cls._check_pow2(every.t(), codes_t, 128, rows)
+            else:
+                cls._check_pow2(scales[:, :rows].t(), codes, 1, cols)
+                if codes_t is not None and scales_t is not None:
+                    cls._check_pow2(scales_t[:, :cols].t(), codes_t, 1, rows)
         self._set(rows, cols, shape, scale, codes, codes_t, scales, scales_t)
         return self
+
+    @staticmethod
+    def _check_pow2(scales, codes, height, cols):
+        """Scales of blocks of height x 128 codes whose exponents alone tell them."""
+        zero = scales == 0
+        power = (scales.view(torch.int32) & 0x7FFFFF == 0) & (scales >= 2.0 ** -126) & scales.isfinite()
+        if not bool((power | zero | scales.isnan()).all()):
+            raise ValueError("scales of kind POW2 must be powers of two, at least 2^-126")
+        if bool(zero.any()):
+            under = zero.repeat_interleave(height, 0)[:codes.shape[0]].repeat_interleave(128, 1)
+            if bool((codes[:, :cols] & 0x7F)[under[:, :cols]].any()):
+                raise ValueError("codes under a scale of 0 (kind POW2) must be zero")
 
     def quantize(self, src, stream=None):
         """hq_block_quantize of src (rows x cols, contiguous) into these buffers."""

@@ -71,8 +71,8 @@ typedef enum { HQ_BSCALE_F32 = 0, HQ_BSCALE_POW2 = 1 } hq_block_scale;
  * Bytes of a code row from its length to the next multiple of 16 are zero (the producer writes
  * them; a caller that brings codes of its own keeps this rule).
  * rows, cols, shape and scale are written by hq_block_quantize and checked by every consumer.
- * A tensor with scale = POW2 promises that every scale is 0, NaN or a power of two: the products
- * read its exponent alone. */
+ * A tensor with scale = POW2 promises that every scale is a power of two from 2^-126 up, NaN, or 0
+ * with zero codes, as the quantizer writes them: the products may read its exponent alone. */
 typedef struct {
   uint8_t *codes;
   uint8_t *codes_t;

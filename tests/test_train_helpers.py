@@ -161,3 +161,49 @@ def test_block_tensor_keeps_its_buffers(name):
         with pytest.raises(AttributeError):
             setattr(q, name, torch.zeros(3))
         assert getattr(q, name) is old
+
+
+def wrapped(shape, codes, codes_t, scales, scales_t, rows=200, cols=300):
+    return T.BlockTensor.wrap(codes, scales, rows, cols, shape=shape, scale=B.HQ_BSCALE_POW2,
+                              codes_t=codes_t, scales_t=scales_t)
+
+
+def pow2_parts(shape):
+    """Codes in both layouts and scales of 200 x 300 elements, with room behind what is read."""
+    codes = torch.full((200, 320), 0x38, dtype=torch.uint8)
+    codes_t = torch.full((300, 224), 0x38, dtype=torch.uint8)
+    if shape == B.HQ_BLOCK_TILES:
+        return codes, codes_t, torch.full((2, 5), 0.25), None
+    return codes, codes_t, torch.full((3, 210), 0.25), torch.full((2, 310), 0.25)
+
+
+@pytest.mark.parametrize("shape", [B.HQ_BLOCK_ROWS, B.HQ_BLOCK_TILES])
+@pytest.mark.parametrize("bad", [3.0, -0.5, float("inf"), 2.0 ** -127, 2.0 ** -130, 2.0 ** -149, 0.0])
+def test_wrap_refuses_scales_that_the_exponent_does_not_tell(shape, bad):
+    """A power-of-two product reads a scale's exponent alone: a subnormal scale, or zero over codes
+    that are not zero, would count as 2^-127."""
+    for which in (2, 3) if shape == B.HQ_BLOCK_ROWS else (2,):
+        parts = pow2_parts(shape)
+        wrapped(shape, *parts)
+        parts[which][1, 2] = bad
+        with pytest.raises(ValueError, match="POW2"):
+            wrapped(shape, *parts)
+
+
+@pytest.mark.parametrize("shape", [B.HQ_BLOCK_ROWS, B.HQ_BLOCK_TILES])
+def test_wrap_takes_every_scale_that_it_promises(shape):
+    """From 2^-126 up, NaN, and zero over zero codes of either sign; what is behind is not read."""
+    codes, codes_t, scales, scales_t = pow2_parts(shape)
+    scales[0, 0], scales[0, 1], scales[1, 1] = 2.0 ** -126, 2.0 ** 127, float("nan")
+    if shape == B.HQ_BLOCK_TILES:
+        scales[1, 2] = 0.0
+        codes[128:, 256:300], codes_t[256:, 128:200] = 0x80, 0
+        scales[:, 3:] = 3.0
+    else:
+        scales[2, 7] = scales_t[1, 9] = 0.0
+        codes[7, 256:300], codes_t[9, 128:200] = 0x80, 0
+        scales[:, 200:] = scales_t[:, 300:] = 3.0
+    wrapped(shape, codes, codes_t, scales, scales_t)
+    codes_t[-1 if shape == B.HQ_BLOCK_TILES else 9, 199] = 1    # one code under a zero scale
+    with pytest.raises(ValueError, match="POW2"):
+        wrapped(shape, codes, codes_t, scales, scales_t)
