@@ -124,12 +124,6 @@ __device__ inline void bcast16_first8(float x, float (&r)[8]) {
   r[4] = bcast16<4>(x); r[5] = bcast16<5>(x); r[6] = bcast16<6>(x); r[7] = bcast16<7>(x);
 }
 
-// Eight codes; r = 0 stands for a block of zeros or one that is not finite: zero codes.
-__device__ inline uint2 codes8_or0(const float (&v)[8], float r) {
-  const uint2 q = {e4m3_codes4(v[0], v[1], v[2], v[3], r), e4m3_codes4(v[4], v[5], v[6], v[7], r)};
-  return r != 0.0f ? q : uint2{0u, 0u};
-}
-
 template <class T, bool TILES>
 __global__ __launch_bounds__(256) void block_quant_kernel(BlockQuantArgs g) {
   __shared__ uint32_t cmax[4][128];
@@ -180,7 +174,7 @@ __global__ __launch_bounds__(256) void block_quant_kernel(BlockQuantArgs g) {
       float v[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = x.value(i, j);
-      const uint2 q = codes8_or0(v, rr[i]);
+      const uint2 q = e4m3_codes8(v, rr[i]);
       if (row0 + i < g.rows && in) *reinterpret_cast<uint2*>(g.codes + (row0 + i) * g.ld + col0) = q;
     }
   }
@@ -213,7 +207,7 @@ __global__ __launch_bounds__(256) void block_quant_kernel(BlockQuantArgs g) {
     float v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = x.value(i, j);
-    *reinterpret_cast<uint2*>(&turned[(8 * cg + j) * 128 + 8 * (rg ^ (2 * (cg & 7)))]) = codes8_or0(v, rc[j]);
+    *reinterpret_cast<uint2*>(&turned[(8 * cg + j) * 128 + 8 * (rg ^ (2 * (cg & 7)))]) = e4m3_codes8(v, rc[j]);
   }
   __syncthreads();
   // 8 lanes cover the 128 codes of a transposed row
@@ -246,7 +240,7 @@ __global__ __launch_bounds__(256) void block_quant_rows_kernel(BlockQuantArgs g)
     block_scale(max16(mag8(v[i])), g.pow2, s, r);
     if (row0 + i >= g.rows) continue;
     if (col0 < ((g.cols + 15) & ~int64_t{15}))
-      *reinterpret_cast<uint2*>(g.codes + (row0 + i) * g.ld + col0) = e4m3_codes8(v[i], s, r);
+      *reinterpret_cast<uint2*>(g.codes + (row0 + i) * g.ld + col0) = e4m3_codes8(v[i], r);
     if ((t & 15) == 0 && n > 0) g.scales[(col0 >> 7) * g.lds + row0 + i] = s;
   }
 }

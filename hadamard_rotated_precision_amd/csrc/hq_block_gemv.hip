@@ -51,7 +51,7 @@ __device__ inline void quantize_tokens(const GemvArgs& g, int kpad, uint8_t* cod
   auto put = [&](int m, int c, const float (&v)[8]) {
     float s, r;
     block_scale(max16(mag8(v)), g.pow2, s, r);
-    *reinterpret_cast<uint2*>(codes + m * kpad + c) = e4m3_codes8(v, s, r);
+    *reinterpret_cast<uint2*>(codes + m * kpad + c) = e4m3_codes8(v, r);
     if ((threadIdx.x & 15) == 0) scales[m * (kpad >> 7) + (c >> 7)] = s;
   };
   for (int c = 8 * threadIdx.x; c < kpad; c += 8 * 64 * kGvWaves) {

@@ -138,12 +138,11 @@ __device__ inline uint32_t e4m3_codes4(float a, float b, float c, float d, float
   w = __builtin_amdgcn_cvt_pk_fp8_f32(c * r, d * r, w, true);
   return static_cast<uint32_t>(w);
 }
-// Eight codes; zeros in a block with a NaN scale.
-__device__ inline uint2 e4m3_codes8(const float (&v)[8], float s, float r) {
-  uint2 q;
-  q.x = e4m3_codes4(v[0], v[1], v[2], v[3], r);
-  q.y = e4m3_codes4(v[4], v[5], v[6], v[7], r);
-  return s == s ? q : uint2{0u, 0u};
+// Eight codes. r = 0 stands for a block of zeros (of either sign) or one that is not finite: zero
+// bytes.
+__device__ inline uint2 e4m3_codes8(const float (&v)[8], float r) {
+  const uint2 q = {e4m3_codes4(v[0], v[1], v[2], v[3], r), e4m3_codes4(v[4], v[5], v[6], v[7], r)};
+  return r != 0.0f ? q : uint2{0u, 0u};
 }
 
 // ---------------------------------------------------------------- products of one block of K

@@ -628,3 +628,23 @@ def test_gemm_outputs_of_many_rounds(M, N, K):
         va, vb = as_values(a)[rows].contiguous(), as_values(b)
         want = torch.mm(va, vb.t().contiguous())
         R.assert_within(c[rows], want, R.product_bound(va, vb, want, dtype), "sampled rows")
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("kind", [F32, POW2])
+def test_blocks_of_zeros_have_zero_bytes(kind, dtype):
+    """Blocks of +0 and -0, and one that is not finite: code bytes 0x00 from every kernel, and the
+    same bytes whichever layouts are asked for."""
+    for rows, cols in ((1, 128), (3, 300), (40, 1000), (300, 260), (5000, 140)):
+        x = draw(gen(rows), rows, cols, dtype)
+        zero = torch.rand(rows, cols, generator=gen(1), device=DEV) < 0.5
+        x[:, :128] = torch.where(zero, -0.0, 0.0)[:, :128]
+        x[rows // 2, -1] = float("inf")
+        for shape in (ROWS, TILES):
+            both = T.BlockTensor(rows, cols, shape=shape, scale=kind).quantize(x)
+            assert not both.codes[:, :128].any() and not both.codes_t[:128].any()
+            for kw in (dict(codes=False), dict(codes_t=False)):
+                one = T.BlockTensor(rows, cols, shape=shape, scale=kind, **kw).quantize(x)
+                for name in ("codes", "codes_t"):
+                    if getattr(one, name) is not None:
+                        assert torch.equal(getattr(one, name), getattr(both, name)), (rows, cols, shape, name)
