@@ -103,6 +103,11 @@ hq_status hq_block_quantize(const void *src, int32_t src_dtype, int64_t rows, in
  * cuts the others 13 bits below, and adds the groups in fp32. On normally distributed data that is
  * a relative error of about 1.5e-5 of the result, against 2e-4 of an fp16 and 2e-3 of a bf16
  * output's own rounding.
+ * Scales: sa sb is formed in fp32 before it meets the block's sum. While it is at least 2^-126 the
+ * above holds. A smaller one has a step of 2^-149: an error of at most 2^-150 times the sum of the
+ * block's |a b|, so below 2^-125. From 2^128 on it is infinite, and the outputs that read the block
+ * are infinite or NaN. (Two POW2 tensors with 16-bit outputs may escape either limit: the
+ * instruction then adds their exponents.)
  * Workspace: hq_block_gemm_workspace_bytes(M, N, K) bytes; 0 (and NULL) for many shapes. */
 typedef enum { HQ_SIDE_ROWS = 0, HQ_SIDE_COLS = 1 } hq_block_side;
 

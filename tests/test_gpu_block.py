@@ -648,3 +648,47 @@ def test_blocks_of_zeros_have_zero_bytes(kind, dtype):
                 for name in ("codes", "codes_t"):
                     if getattr(one, name) is not None:
                         assert torch.equal(getattr(one, name), getattr(both, name)), (rows, cols, shape, name)
+
+
+def scaled_codes(g, rows, cols, shape, kind, low, high):
+    """Random codes with scales between 2^low and 2^high, as a BlockTensor, and both as fp64."""
+    codes = torch.zeros(rows, (cols + 15) // 16 * 16, dtype=torch.uint8, device=DEV)
+    q, _ = R.quantize(torch.randn(rows, cols, generator=g, device=DEV), 1, 128)
+    codes[:, :cols] = q.to(R.E4M3).view(torch.uint8)
+    rb, cb = -(-rows // 128), -(-cols // 128)
+    e = torch.rand((cb, rows) if shape == ROWS else (rb, cb), generator=g, device=DEV) * (high - low) + low
+    s = torch.exp2(e.floor() if kind == POW2 else e)
+    each = R.spread(s.double().t().contiguous() if shape == ROWS else s.double(),
+                    1 if shape == ROWS else 128, 1, (rows, cb))      # rows x blocks of K
+    return T.BlockTensor.wrap(codes, s, rows, cols, shape=shape, scale=kind), q, each
+
+
+@pytest.mark.parametrize("lows", [(-85, -65), (-126, -20), (-20, -126), (20, 30), (40, 45)])
+@pytest.mark.parametrize("M,N,K", [(3, 300, 500), (30, 70, 260), (100, 300, 700), (40, 60, 8192), (1001, 4100, 260),
+                                   (1100, 13900, 130)])
+def test_scales_whose_product_is_small_or_large(M, N, K, lows):
+    """sa sb is formed in fp32: relative accuracy while it is at least 2^-126, and below that an
+    error of half a subnormal step, 2^-150, times the sum of the block's products of codes."""
+    for k, (dtype, kinds, shapes) in enumerate([
+            (torch.float32, (F32, F32), (ROWS, TILES)), (torch.bfloat16, (F32, F32), (ROWS, TILES)),
+            (torch.bfloat16, (F32, F32), (ROWS, ROWS)), (torch.float32, (POW2, F32), (TILES, ROWS)),
+            (torch.bfloat16, (POW2, POW2), (ROWS, TILES))]):
+        print("[case] gemm", M, N, K, lows, dtype, kinds, shapes, flush=True)
+        g = gen(M + K + k)
+        (a, qa, sa), (b, qb, sb) = (scaled_codes(g, r, K, s, kind, lo, lo + 20)
+                                    for r, s, kind, lo in ((M, shapes[0], kinds[0], lows[0]),
+                                                           (N, shapes[1], kinds[1], lows[1])))
+        c = torch.empty(M, N, dtype=dtype, device=DEV)
+        T.block_gemm(a, b, c)
+        va, vb = (q * s[:, torch.arange(K, device=DEV) // 128] for q, s in ((qa, sa), (qb, sb)))
+        want = torch.mm(va, vb.t().contiguous())
+        bound = R.product_bound(va, vb, want, dtype)
+        for kb in range(sa.shape[1]):
+            at = slice(128 * kb, 128 * kb + 128)
+            few = torch.outer(sa[:, kb], sb[:, kb]) < 2.0 ** -126
+            bound += few * 2.0 ** -150 * torch.mm(qa[:, at].abs(), qb[:, at].abs().t().contiguous())
+        # sum |a b| bounds every partial sum and the result: below fp32's range they all are finite;
+        # past it they need not be (scales of 2^60 and 2^65, codes up to 2^8.8 each: 2^142)
+        fits = torch.mm(va.abs(), vb.abs().t().contiguous()) < 2.0 ** 127
+        assert c[fits].isfinite().all()
+        R.assert_within(c[fits], want[fits], bound[fits], "small scales")
