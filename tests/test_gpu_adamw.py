@@ -491,3 +491,86 @@ def test_captured_steps_run_ahead_on_a_stream_of_their_own(bits):
     assert torch.equal(p, q)
     for name in eager.states[0]:
         assert torch.equal(eager.states[0][name], taken.states[0][name])
+
+
+@pytest.mark.parametrize("value", [2e-5, 6e-6])
+def test_8_bit_rounding_is_unbiased_among_subnormal_codes(value):
+    """Beside a block's largest of 1 these are 4.6 and 1.4 steps of the subnormal codes (2^-9), so
+    the codes 4 and 5, or 1 and 2: each appears, and the means of m and of v are the values, within
+    five standard deviations, the 2^-16 grain of the probabilities and the fp32 errors of x (2^-20)."""
+    n = 128 * 2000
+    grad = torch.full((n,), value, device=DEV)
+    grad[::128] = 1.0
+    opt = T.AdamW([torch.zeros(n, device=DEV)], lr=1e-3, betas=(0.0, 0.0), state_bits=8, seed=1)
+    opt.step([grad])
+    keep = torch.ones(n, dtype=torch.bool, device=DEV)
+    keep[::128] = False
+    x = value * 448
+    low = math.floor(x * 512)
+    assert x < 2.0 ** -6
+    for name, got, power in zip("mv", eight_bit_values(opt.states[0], n), (1, 2)):
+        assert sorted(opt.states[0][name][keep].unique().tolist()) == [low, low + 1]
+        got, want = got[keep], float(grad[1]) ** power
+        gap = (((low + 1) ** power - low ** power) / 512.0 ** power) / 448.0 ** power
+        spread = float(got.std())
+        off = abs(float(got.mean()) - want)
+        print("[mean] %s %g: off by %.3g, five deviations %.3g" % (name, value, off, 5 * spread / math.sqrt(got.numel())), flush=True)
+        assert off <= 5 * spread / math.sqrt(got.numel()) + 2.0 ** -16 * gap + 2.0 ** -20 * want
+
+
+def test_subnormal_codes_follow_the_documented_random_numbers():
+    """Every element whose fraction is away from the border (2^-10: the grain of 2^-16 and the fp32
+    errors of x are below it) rounds as its random number says, v from the first code up."""
+    n, seed, step = 128 * 300, 77, 9
+    g = gen(31)
+    grad = randn(g, n) * torch.exp2(-6 - 10 * torch.rand(n, generator=g, device=DEV)) / 448
+    grad[::128] = 1.0
+    opt = T.AdamW([torch.zeros(1, device=DEV), torch.zeros(n, device=DEV)], lr=1e-3, betas=(0.0, 0.0),
+                  state_bits=8, seed=seed, steps_done=step - 1)
+    opt.step([torch.zeros(1, device=DEV), grad])
+    st, tensor = opt.states[1], 1
+
+    def mix(h):
+        for shift, factor in ((16, 2654435761), (15, 2891336453), (16, 1)):
+            h = ((h ^ (h >> shift)) * factor) & 0xFFFFFFFF
+        return h
+
+    key = int(mix(torch.tensor((seed + 2654435761 * step) & 0xFFFFFFFF))) + 0x9E3779B9 * (tensor + 1)
+    i = torch.arange(n, device=DEV)
+    u = mix(i ^ (key & 0xFFFFFFFF))
+    assert (int(u[5]) & 0xFFFF, int(u[5]) >> 16) == random_of(seed, step, tensor, 5)
+    for name, r in (("m", u & 0xFFFF), ("v", u >> 16)):
+        r = r.double() / 65536
+        x = grad.double().abs() / st[name + "_scales"].double()[i // 128]
+        low, high = neighbours(x)
+        if name == "m":
+            border = 1 - (x - low) / (high - low)
+            up = r >= border
+        else:
+            border = (x * x - low * low) / (high * high - low * low)
+            up = r < border
+        tested = (x < 2.0 ** -6) & ((r - border).abs() > 2.0 ** -10)
+        if name == "v":
+            tested &= x >= 2.0 ** -9
+        got = st[name].view(R.E4M3).double().abs()
+        assert torch.equal(got[tested], torch.where(up, high, low)[tested]), name
+        codes = st[name][tested] & 0x7F
+        # of ten octaves of x the three from the first code up to 2^-6 count for v
+        assert int(tested.sum()) > n // 8 and set(range(1, 8)) <= set(codes.unique().tolist())
+
+
+def test_every_significand_of_the_denominator():
+    """The update's 1 / den is the correctly rounded one for each of the 2^23 significands. With
+    beta1 = 1/2, beta2 = 1/4, no gradient and states m = 2, v = 4 y^2: m becomes 1 and v y^2, whose
+    rounded root is y again; far on, both bias corrections are 1, eps is lost beside y, and p = 0
+    becomes -1 / y (lr 1, no decay)."""
+    y = torch.arange(0x3F800000, 0x40000000, dtype=torch.int32, device=DEV).view(torch.float32)
+    n = y.numel()
+    root = (y * y).double().sqrt().float()
+    assert torch.equal(root, y)
+    p = torch.zeros(n, device=DEV)
+    st = {"m": torch.full((n,), 2.0, device=DEV), "v": 4.0 * (y * y)}
+    opt = T.AdamW([p], lr=1.0, betas=(0.5, 0.25), eps=1.2e-38, weight_decay=0.0, states=[st], steps_done=999)
+    opt.step([torch.zeros(n, device=DEV)])
+    assert (st["m"] == 1).all() and torch.equal(st["v"], y * y)
+    assert torch.equal(p, -y.double().reciprocal().float())

@@ -692,3 +692,19 @@ def test_scales_whose_product_is_small_or_large(M, N, K, lows):
         fits = torch.mm(va.abs(), vb.abs().t().contiguous()) < 2.0 ** 127
         assert c[fits].isfinite().all()
         R.assert_within(c[fits], want[fits], bound[fits], "small scales")
+
+
+@pytest.mark.parametrize("exponent", [-126, -117, -40, 0, 100, 127])
+def test_scales_of_every_significand(exponent):
+    """s = fp32(a / 448) and the code of a, for each of the 2^23 significands of a: one value to a
+    block. (The fp64 quotient of fp32 numbers rounds to the correctly rounded one.)"""
+    first = (exponent + 127) << 23
+    a = torch.arange(first, first + (1 << 23), dtype=torch.int32, device=DEV).view(torch.float32)
+    a[1::2] *= -1
+    for part in a.split(1 << 22):
+        x = part.view(-1, 1)
+        for kind in (F32, POW2):
+            q = T.BlockTensor(x.shape[0], 1, scale=kind, codes_t=False).quantize(x)
+            want, s = R.quantize(x, 1, 128, kind)
+            assert torch.equal(q.scales.double().view(-1), s.view(-1))
+            assert torch.equal(q.codes_view().view(R.E4M3).double(), want)
