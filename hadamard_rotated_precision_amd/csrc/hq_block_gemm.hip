@@ -28,8 +28,6 @@
 // waves of 128 x 128 with accumulators in AGPRs (spills), fragments two rows ahead, double-buffered
 // fragments and four stages for the small tiles, a tail of half tiles for a partly filled last
 // round (5 % alone, nothing within a training step: the clock rises when units idle).
-#include <type_traits>
-
 #include "hq_device.hpp"
 #include "hq_launch.hpp"
 #include "hq_train_device.hpp"
@@ -38,10 +36,8 @@
 namespace hq {
 
 typedef float v4f __attribute__((ext_vector_type(4)));
-typedef float v16f __attribute__((ext_vector_type(16)));
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v8i __attribute__((ext_vector_type(8)));
-typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 
 constexpr int kFar = 0x7FFFFFF0;   // an offset past any descriptor: the load reads 0

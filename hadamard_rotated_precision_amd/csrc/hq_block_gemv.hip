@@ -25,7 +25,6 @@ namespace hq {
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
-typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 
 constexpr int kGvWaves = 8;
 constexpr int kGvAhead = 2;              // blocks of K in flight per wave

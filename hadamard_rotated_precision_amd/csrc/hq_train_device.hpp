@@ -1,6 +1,7 @@
-// hq_train_device.hpp — element access shared by the kernels of include/hq_train.h: groups of
-// eight consecutive elements, whole and aligned ones with wide accesses. Stores keep NaN (the
-// shared bf16 store of hq_device.hpp takes finite values only).
+// hq_train_device.hpp — device helpers shared by the kernels of include/hq_train.h: groups of eight
+// consecutive elements (whole ones with wide accesses, at any alignment; stores keep NaN, where the
+// bf16 store of hq_device.hpp takes finite values only), block scales and codes, and the products
+// of one block of K.
 #pragma once
 
 #include "hq_device.hpp"

@@ -10,8 +10,6 @@
 
 namespace hq {
 
-constexpr int kBlk = HQ_BLOCK;
-
 // Block quantizer (hq_block.hip). codes or codes_t may be null, not both.
 struct BlockQuantPass {
   const void* src = nullptr;
@@ -47,7 +45,6 @@ struct BlockGemmPass {
   int out_dt = 0;
   bool accumulate = false;
   void* ws = nullptr;
-  int cus = 256;
 };
 size_t block_gemm_ws(int64_t M, int64_t N, int64_t K);
 hipError_t block_gemm_pass(const BlockGemmPass& p, hipStream_t st);
