@@ -190,11 +190,17 @@ __global__ __launch_bounds__(64 * kGvWaves) void block_gemv_kernel(GemvArgs g) {
   }
 }
 
-// Up to 16 tokens; 17 to 32 while b is small (4096 x 4096 at 17 tokens: 9.7 us against 12.1 on
-// 64 x 64 tiles with K split; 4096 x 11008 at 32: 20.9 against 17.6, each with the tokens'
-// quantization), for the tokens' codes are read again by every workgroup.
+// Up to 16 tokens; 17 to 32 while every compute unit gets one workgroup at most (N <= 16 x 256) and
+// the tokens are few and short enough, for each workgroup reads all of their codes: M K up to 3 2^16.
+// Against 64 x 64 tiles with K split, us at 17 / 24 / 32 tokens, this form first (N x K):
+//   4096 x 4096: 8.0 8.7 9.3 / 10.9 11.1 11.2       1024 x 4096: 7.2 7.9 8.5 / 11.5 12.0 12.4
+//   4096 x 6400: 9.8 11.1 12.2 / 13.3 13.6 13.7     2048 x 6400: 9.4 10.6 11.8 / 11.5 11.5 11.7
+//   4096 x 8192: 11.3 12.7 14.4 / 13.3 13.6 13.5    1024 x 8192: 11.2 12.6 14.6 / 12.0 12.9 13.0
+//   1024 x 16384: 19.2 21.8 24.9 / 14.2 14.8 14.6   (M K at 32 tokens: 3.1 2^16 for K = 6400)
+// and with two rounds of workgroups: 4112 x 4096: 12.2 13.4 14.7 / 11.9 12.0 12.1,
+//   4112 x 11008: 25.2 28.7 32.2 / 16.7 17.0 17.4,  16384 x 1024: 8.5 8.9 9.3 / 7.5 7.5 7.5.
 bool block_gemv_ok(int64_t M, int64_t N, int64_t K) {
-  return M >= 1 && K >= 1 && (M <= 16 || (M <= 32 && N * K <= int64_t{1} << 24));
+  return M >= 1 && K >= 1 && (M <= 16 || (M <= 32 && N <= 16 * 256 && M * K <= int64_t{3} << 16));
 }
 
 // Fused when the tokens' codes fit their LDS. Every workgroup repeats the quantizing: past that a
@@ -219,10 +225,9 @@ static hipError_t launch_rows(const GemvArgs& a, bool fused, hipStream_t st, int
   // 16 rows of b per workgroup while all workgroups are on the chip at once (three to a compute
   // unit), else 32: one token at 4096 x 11008 takes 11.5 against 12.6 us, at 5120 x 13824 15.8
   // against 13.8
-  const bool two = a.N > 16 * 3 * 256;
-  if (a.M <= 16)
-    return two ? launch_gemv<Out, 2, 1, P_ROWS, EXACT>(a, fused, st, tok) : launch_gemv<Out, 1, 1, P_ROWS, EXACT>(a, fused, st, tok);
-  return two ? launch_gemv<Out, 2, 2, P_ROWS, EXACT>(a, fused, st, tok) : launch_gemv<Out, 1, 2, P_ROWS, EXACT>(a, fused, st, tok);
+  if (a.M > 16) return launch_gemv<Out, 1, 2, P_ROWS, EXACT>(a, fused, st, tok);
+  return a.N > 16 * 3 * 256 ? launch_gemv<Out, 2, 1, P_ROWS, EXACT>(a, fused, st, tok)
+                            : launch_gemv<Out, 1, 1, P_ROWS, EXACT>(a, fused, st, tok);
 }
 
 template <class Out, bool EXACT>

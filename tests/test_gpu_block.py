@@ -789,3 +789,19 @@ def test_sums_of_data_with_outliers_follow_the_stated_rule(M, N, K, kind):
         T.block_gemm(a, b, c)
         bound = sums + R.HALF_STEP[dtype] * (want.abs() + sums) + (2.0 ** -25 if dtype == torch.float16 else 2.0 ** -126)
         R.assert_within(c[rows], want, bound, "rule")
+
+
+@pytest.mark.parametrize("M,N,K", [(17, 4096, 8192), (32, 4096, 6144), (32, 1500, 6100), (17, 4097, 512), (32, 1024, 16384),
+                                   (24, 16500, 300)])
+def test_few_rows_on_either_side_of_the_rule(M, N, K):
+    """17 to 32 rows, on the form without tiles and beside its limits."""
+    for k, (dtype, kinds, shapes) in enumerate([
+            (torch.bfloat16, (F32, F32), (ROWS, TILES)), (torch.float16, (POW2, POW2), (ROWS, TILES)),
+            (torch.bfloat16, (F32, F32), (TILES, ROWS)), (torch.float32, (F32, F32), (ROWS, ROWS))]):
+        print("[case] gemm", M, N, K, dtype, kinds, shapes, flush=True)
+        a, b = operands(M, N, K, kinds, shapes, k)
+        c = torch.full((M, N), float("nan"), dtype=dtype, device=DEV)
+        T.block_gemm(a, b, c)
+        va, vb = as_values(a), as_values(b)
+        want = torch.mm(va, vb.t().contiguous())
+        R.assert_within(c, want, R.product_bound(va, vb, want, dtype), "few rows")

@@ -207,3 +207,12 @@ def test_wrap_takes_every_scale_that_it_promises(shape):
     codes_t[-1 if shape == B.HQ_BLOCK_TILES else 9, 199] = 1    # one code under a zero scale
     with pytest.raises(ValueError, match="POW2"):
         wrapped(shape, codes, codes_t, scales, scales_t)
+
+
+@pytest.mark.parametrize("M,N,K,split", [(32, 1024, 16384, True), (17, 1024, 16384, True), (24, 4112, 4096, True),
+                                         (17, 4096, 8192, False), (32, 4096, 6144, False), (32, 1024, 4096, False),
+                                         (16, 1024, 16384, False)])
+def test_few_tokens_split_a_long_contraction(M, N, K, split):
+    """17 to 32 tokens against long or wide weights run on tiles with K split, whose sums need a
+    workspace; the few-token form, which needs none, reads every token in every workgroup."""
+    assert (B.hq_block_gemm_workspace_bytes(M, N, K) > 0) == split
