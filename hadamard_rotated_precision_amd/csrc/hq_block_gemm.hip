@@ -484,14 +484,11 @@ static hipError_t launch_mode(BlockGemmArgs a, hipStream_t st, int tok) {
     default:
       if constexpr (!EXACT) {
         // rows held over the barrier: more of them lengthen the stretch in which the next loads are
-        // issued one by one, which costs less of the clock on long runs (8192 x 13824 x 5120: 470 us
-        // with three, 482 with two; 4096^3 back to back: 62.4 against 63.6); a single round of
-        // workgroups after other work waits for its loads instead (1000 tokens at 5120 x 13824 with
-        // their quantization: 71.4 against 69.0)
-        if constexpr (MODE == S_TILES) {
-          if (((a.M + 255) / 256) * ((a.N + 255) / 256) <= 256)
-            return launch_tiled<Out, MODE, EXACT, 2, 4, 8, 4, 2, 1>(a, st, tok);
-        }
+        // issued one by one. Three against two, tile scales, M x N x K outputs and contraction:
+        // 8192 x 5120 x 13824 480 / 484 us, 4096 x 11008 x 4096 162 / 164, 4096^3 58.2 / 59.3,
+        // 3500 x 4096 x 11008 134 / 135; of ten shapes of a single round of workgroups with their
+        // tokens' quantization eight gain up to 2 %, 1792 x 8960 x 2000 loses 1.5 %, and
+        // 1000 x 13824 x 5120 gained 1 % on one card and lost 1.5 % on another
         return launch_tiled<Out, MODE, EXACT, 2, 4, 8, 4, MODE == S_POW2 ? 4 : 3, 1>(a, st, tok);
       }
   }
