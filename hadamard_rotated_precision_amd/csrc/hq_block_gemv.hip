@@ -2,14 +2,16 @@
 //   c[m][n] (+)= sum_kb sa(m,kb) sb(n,kb) sum_{k in kb} a[m][k] b[n][k]
 //
 // What bounds it: the bytes of b, read once, and about 3 us of launch, first loads and joining. One
-// token takes 11.5 us at 4096 x 11008 (45 MB: 3.9 TB/s, 5.9 TB/s past those 3 us), 6.3 at 4096 x
+// token takes 11.5 us at 4096 x 11008 (45 MB: 3.9 TB/s, 5.3 TB/s past those 3 us), 6.3 at 4096 x
 // 4096, 13.8 at 5120 x 13824 (5.1 TB/s). Four blocks ahead instead of two, four or sixteen waves
 // instead of eight: equal or slower. A workgroup takes 16 RT rows of b and the whole
 // contraction; its eight waves take every eighth block of 128 K each, so that together they read
 // 1 KB of every row at a time. A wave's fragments come straight from memory into the operand
 // registers (16 rows x 64 contiguous bytes per load), two blocks ahead of their use; the tokens
 // are the lanes' side of v_mfma_f32_16x16x128_f8f6f4, padded to 16 or 32 with zeros. The eight partial
-// sums meet in LDS and are added in the order of the waves.
+// sums meet in LDS and are added in the order of the waves. 16-bit outputs take the FP8 instruction
+// here too (its error: hq_block_gemm.hip); the exact sums of fp32 outputs cost up to 2 % with one
+// token and 1 to 5 % with 13 to 16 (16 tokens at 5120 x 13824: 23.4 against 22.3 us).
 //
 // The tokens come as codes, or (fused, for few enough elements) as the caller's own values:
 // then every workgroup quantizes them into LDS while its first rows of b are on their way.

@@ -106,10 +106,9 @@ __device__ inline uint32_t max16(uint32_t x) {
 }
 
 // x / 448 and 1 / x, correctly rounded, in three operations each instead of the dozen of a
-// division: an estimate within one unit, its exact remainder by one fma, and a correction. The
-// quotient was checked against the division for every significand (the exponent does not matter
-// above 2^-117, where the remainder is a normal or an exact subnormal number), the reciprocal for
-// every significand on the GPU.
+// division: an estimate within one unit, its exact remainder by one fma, and a correction. Both are
+// tested on the GPU for every significand (the exponent does not matter to the quotient above
+// 2^-117, where the remainder is a normal or an exact subnormal number).
 __device__ inline float div448(float x) {
   constexpr float c = 1.0f / 448.0f;
   const float q = x * c;
