@@ -2,8 +2,9 @@
 //   c[m][n] (+)= sum_kb sa(m,kb) sb(n,kb) sum_{k in kb} a[m][k] b[n][k]
 //
 // What bounds it: the bytes of b, read once, and about 3 us of launch, first loads and joining. One
-// token takes 11.5 us at 4096 x 11008 (45 MB: 3.9 TB/s, 5.3 TB/s past those 3 us), 6.3 at 4096 x
-// 4096, 13.8 at 5120 x 13824 (5.1 TB/s). Four blocks ahead instead of two, four or sixteen waves
+// token takes 11.5 us at 4096 x 11008 with the weights in the 256 MB cache before the memory (45 MB:
+// 3.9 TB/s, 5.3 TB/s past those 3 us) and 12.4 us from memory, 6.2 and 7.4 at 4096 x 4096, 13.4 and
+// 16 at 5120 x 13824 (5.3 and 4.4 TB/s). Four blocks ahead instead of two, four or sixteen waves
 // instead of eight: equal or slower. A workgroup takes 16 RT rows of b and the whole
 // contraction; its eight waves take every eighth block of 128 K each, so that together they read
 // 1 KB of every row at a time. A wave's fragments come straight from memory into the operand
@@ -225,8 +226,10 @@ static hipError_t launch_gemv(const GemvArgs& a, bool fused, hipStream_t st, int
 template <class Out, bool P_ROWS, bool EXACT>
 static hipError_t launch_rows(const GemvArgs& a, bool fused, hipStream_t st, int tok) {
   // 16 rows of b per workgroup while all workgroups are on the chip at once (three to a compute
-  // unit), else 32: one token at 4096 x 11008 takes 11.5 against 12.6 us, at 5120 x 13824 15.8
-  // against 13.8
+  // unit), else 32. One token, weights from memory, 16 / 32 rows (N x K): 1024 x 4096 6.5 / 8.6 us,
+  // 11008 x 4096 13.8 / 14.0, 4096 x 11008 14.9 / 16.9; 13824 x 5120 17.6 / 15.7, 16384 x 1024
+  // 7.8 / 6.6, 32000 x 4096 32.5 / 29.8. (Against the rule: 5120 x 13824 20.1 / 18.4, 20000 x 2048
+  // 11.4 / 12.3.)
   if (a.M > 16) return launch_gemv<Out, 1, 2, P_ROWS, EXACT>(a, fused, st, tok);
   return a.N > 16 * 3 * 256 ? launch_gemv<Out, 2, 1, P_ROWS, EXACT>(a, fused, st, tok)
                             : launch_gemv<Out, 1, 1, P_ROWS, EXACT>(a, fused, st, tok);
