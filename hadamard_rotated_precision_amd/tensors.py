@@ -405,7 +405,7 @@ class AdamW:
 
     Parameters, copies and states may be bound anew (p.data = ..., opt.states[i]["m"] = ...): the
     next step checks them again and works on the new memory. A captured step keeps the addresses of
-    its capture.
+    its capture. Gradients share no memory with what a step writes.
 
     step(grads) takes the next step. Under HIP graph capture a step has to read its scalars from
     device memory: step(grads, captured=True) launches with `device_scalars` (a device tensor of
@@ -490,7 +490,7 @@ class AdamW:
     def _check_overlap(self):
         """All that a step writes has to be disjoint (a copy that is its own parameter aside): a
         parameter listed twice would be updated by two workgroups at once."""
-        written = self.params + [s[k] for s in self.states for k in self._state_keys]
+        written = [*self.params] + [s[k] for s in self.states for k in self._state_keys]
         written += [c for c, p in zip(self.copies or [], self.params) if not self._is_same(c, p)]
         spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
                        for t in written if t.numel())

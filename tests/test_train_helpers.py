@@ -216,3 +216,11 @@ def test_few_tokens_split_a_long_contraction(M, N, K, split):
     """17 to 32 tokens against long or wide weights run on tiles with K split, whose sums need a
     workspace; the few-token form, which needs none, reads every token in every workgroup."""
     assert (B.hq_block_gemm_workspace_bytes(M, N, K) > 0) == split
+
+
+def test_adamw_takes_its_lists_as_tuples(launches):
+    opt, grads = adamw(8, copies=True)
+    opt.params, opt.copies, opt.states = (tuple(t.clone() for t in opt.params), tuple(t.clone() for t in opt.copies),
+                                          tuple({k: t.clone() for k, t in s.items()} for s in opt.states))
+    opt.step(grads)
+    table_is_current(launches[-1], opt)
