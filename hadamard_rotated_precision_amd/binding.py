@@ -1,5 +1,5 @@
-"""Thin ctypes binding of libhq (include/hq.h) and libhq_train (include/hq_train.h): the same
-entry-point names, argument marshalling only. Every step of the computation runs in the HIP kernels behind the C ABI;
+"""Thin ctypes binding of libhq (include/hq.h), libhq_train (include/hq_train.h) and libhq_mx
+(include/hq_mx.h): the same entry-point names, argument marshalling only. Every step of the computation runs in the HIP kernels behind the C ABI;
 torch is used by the helpers below only to allocate device memory and to name streams.
 
 Loading fails loudly when the library is missing and cannot be built: there is no fallback.
@@ -12,6 +12,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 # still no fallback when the named library is missing
 LIB_PATH = os.environ.get("HQ_LIB_PATH") or os.path.join(HERE, "libhq.so")
 TRAIN_LIB_PATH = os.environ.get("HQ_TRAIN_LIB_PATH") or os.path.join(HERE, "libhq_train.so")
+MX_LIB_PATH = os.environ.get("HQ_MX_LIB_PATH") or os.path.join(HERE, "libhq_mx.so")
 
 # enums of include/hq.h
 HQ_OK = 0
@@ -37,6 +38,12 @@ TRAIN_EXPORTS = ["hq_train_abi_version", "hq_block_quantize", "hq_block_gemm_wor
                  "hq_block_gemm", "hq_block_workspace_bytes", "hq_block_linear_fwd",
                  "hq_block_linear_bwd_input", "hq_block_linear_bwd_weight",
                  "hq_adamw_scalars_at", "hq_adamw_step"]
+# entry points of include/hq_mx.h
+MX_EXPORTS = ["hq_mx_abi_version", "hq_mx_quantize", "hq_mx_dequantize",
+              "hq_mx_gemm_workspace_bytes", "hq_mx_gemm", "hq_mx_workspace_bytes",
+              "hq_mx_linear_fwd", "hq_mx_linear_bwd_input", "hq_mx_linear_bwd_weight",
+              "hq_kv_append", "hq_kv_read", "hq_kv_attention_workspace_bytes", "hq_kv_attention"]
+HQ_MX_BLOCK = 32
 HQ_BLOCK = 128
 HQ_BLOCK_ROWS, HQ_BLOCK_TILES = 0, 1
 HQ_BSCALE_F32, HQ_BSCALE_POW2 = 0, 1
@@ -105,6 +112,28 @@ class hq_adamw_scalars(ctypes.Structure):
                 ("key", ctypes.c_uint32)]
 
 
+class hq_mx_tensor(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("codes_t", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p), ("scales_t", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("ld", ctypes.c_int64),
+                ("ld_t", ctypes.c_int64), ("lds", ctypes.c_int64), ("lds_t", ctypes.c_int64),
+                ("rot", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class hq_kv_cache(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("pages", ctypes.c_int64), ("page", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("rot", ctypes.c_int32)]
+
+
+class hq_kv_batch(ctypes.Structure):
+    _fields_ = [("q_starts", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("table_ld", ctypes.c_int64),
+                ("seqs", ctypes.c_int32), ("max_q", ctypes.c_int32), ("max_len", ctypes.c_int32),
+                ("q_heads", ctypes.c_int32), ("window", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
 class HQError(RuntimeError):
     def __init__(self, status, where=""):
         self.status = status
@@ -114,6 +143,7 @@ class HQError(RuntimeError):
 
 _lib = None
 _train_lib = None
+_mx_lib = None
 
 
 def load(build_if_missing=True):
@@ -232,6 +262,42 @@ def load_train():
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = restype, argtypes
     _train_lib = lib
+    return lib
+
+
+def load_mx():
+    """Load libhq_mx.so (after libhq.so, which it links); build all only when it is missing."""
+    global _mx_lib
+    if _mx_lib is not None:
+        return _mx_lib
+    if not os.path.exists(MX_LIB_PATH):
+        from . import build as _build
+        _build.build()
+    load()
+    lib = ctypes.CDLL(MX_LIB_PATH)
+    i32, i64, vp, sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t
+    MT, KC, KB = (ctypes.POINTER(t) for t in (hq_mx_tensor, hq_kv_cache, hq_kv_batch))
+    for name, restype, argtypes in (
+            ("hq_mx_abi_version", i32, []),
+            ("hq_mx_quantize", i32, [vp, i32, i64, i64, i32, vp, MT, vp]),
+            ("hq_mx_dequantize", i32, [MT, i32, vp, i32, vp]),
+            ("hq_mx_gemm_workspace_bytes", sz, [i64, i64, i64]),
+            ("hq_mx_gemm", i32, [MT, i32, MT, i32, vp, i32, i32, vp, sz, vp]),
+            ("hq_mx_workspace_bytes", sz, [i64, i64, i64]),
+            ("hq_mx_linear_fwd", i32,
+             [vp, i32, i64, i64, i64, MT, vp, vp, i32, MT, vp, sz, vp]),
+            ("hq_mx_linear_bwd_input", i32,
+             [vp, i32, i64, i64, i64, MT, vp, vp, i32, MT, vp, sz, vp]),
+            ("hq_mx_linear_bwd_weight", i32,
+             [MT, MT, i64, i64, i64, vp, i32, i32, vp, sz, vp]),
+            ("hq_kv_append", i32, [vp, vp, i32, i64, i64, i64, i64, i64, vp, KC, vp]),
+            ("hq_kv_read", i32, [KC, vp, i64, vp, vp, i32, vp]),
+            ("hq_kv_attention_workspace_bytes", sz, [KC, KB]),
+            ("hq_kv_attention", i32,
+             [vp, i32, i64, i64, i64, KC, KB, vp, i32, vp, vp, sz, vp])):
+        fn = getattr(lib, name)
+        fn.restype, fn.argtypes = restype, argtypes
+    _mx_lib = lib
     return lib
 
 
@@ -406,6 +472,68 @@ def hq_adamw_step(tensors, count, cfg, host_scalars, device_scalars, stream):
     device_scalars: a device pointer or None."""
     return load_train().hq_adamw_step(tensors, count, _ref(cfg), _ref(host_scalars),
                                       device_scalars, stream)
+
+
+# ------------------------------------------------ entry points of include/hq_mx.h
+def hq_mx_abi_version():
+    return load_mx().hq_mx_abi_version()
+
+
+def hq_mx_quantize(src, src_dtype, rows, cols, rot, seed, out, stream):
+    return load_mx().hq_mx_quantize(src, src_dtype, rows, cols, rot, seed, _ref(out), stream)
+
+
+def hq_mx_dequantize(q, side, dst, dst_dtype, stream):
+    return load_mx().hq_mx_dequantize(_ref(q), side, dst, dst_dtype, stream)
+
+
+def hq_mx_gemm_workspace_bytes(M, N, K):
+    return load_mx().hq_mx_gemm_workspace_bytes(M, N, K)
+
+
+def hq_mx_gemm(a, a_side, b, b_side, c, c_dtype, accumulate, ws, ws_bytes, stream):
+    return load_mx().hq_mx_gemm(_ref(a), a_side, _ref(b), b_side, c, c_dtype, accumulate, ws,
+                                ws_bytes, stream)
+
+
+def hq_mx_workspace_bytes(N, C, D):
+    return load_mx().hq_mx_workspace_bytes(N, C, D)
+
+
+def hq_mx_linear_fwd(x, x_dtype, N, C, D, w, seed, y, y_dtype, save_x, ws, ws_bytes, stream):
+    return load_mx().hq_mx_linear_fwd(x, x_dtype, N, C, D, _ref(w), seed, y, y_dtype, _ref(save_x),
+                                      ws, ws_bytes, stream)
+
+
+def hq_mx_linear_bwd_input(dy, dy_dtype, N, C, D, w, seed, dx, dx_dtype, save_g, ws, ws_bytes,
+                           stream):
+    return load_mx().hq_mx_linear_bwd_input(dy, dy_dtype, N, C, D, _ref(w), seed, dx, dx_dtype,
+                                            _ref(save_g), ws, ws_bytes, stream)
+
+
+def hq_mx_linear_bwd_weight(saved_g, saved_x, N, C, D, dw, dw_dtype, accumulate, ws, ws_bytes,
+                            stream):
+    return load_mx().hq_mx_linear_bwd_weight(_ref(saved_g), _ref(saved_x), N, C, D, dw, dw_dtype,
+                                             accumulate, ws, ws_bytes, stream)
+
+
+def hq_kv_append(k, v, dtype, tokens, k_token, k_head, v_token, v_head, slots, cache, stream):
+    return load_mx().hq_kv_append(k, v, dtype, tokens, k_token, k_head, v_token, v_head, slots,
+                                  _ref(cache), stream)
+
+
+def hq_kv_read(cache, slots, n, k_out, v_out, dtype, stream):
+    return load_mx().hq_kv_read(_ref(cache), slots, n, k_out, v_out, dtype, stream)
+
+
+def hq_kv_attention_workspace_bytes(cache, batch):
+    return load_mx().hq_kv_attention_workspace_bytes(_ref(cache), _ref(batch))
+
+
+def hq_kv_attention(q, q_dtype, tokens, q_token, q_head, cache, batch, out, out_dtype, lse, ws,
+                    ws_bytes, stream):
+    return load_mx().hq_kv_attention(q, q_dtype, tokens, q_token, q_head, _ref(cache), _ref(batch),
+                                     out, out_dtype, lse, ws, ws_bytes, stream)
 
 
 def hq_profile_start(kind_mask):

@@ -1,5 +1,5 @@
-"""Build libhq.so (the gfx950 HIP kernels and the C ABI of include/hq.h) and libhq_train.so (those
-of include/hq_train.h) in-tree with hipcc."""
+"""Build libhq.so (the gfx950 HIP kernels and the C ABI of include/hq.h), libhq_train.so (those of
+include/hq_train.h) and libhq_mx.so (those of include/hq_mx.h) in-tree with hipcc."""
 import os
 import subprocess
 import sys
@@ -15,6 +15,10 @@ SOURCES = ["hq_rotate.hip", "hq_prologue.hip", "hq_gemm.hip", "hq_static.hip", "
 TRAIN_LIB = os.path.join(HERE, "libhq_train.so")
 TRAIN_SOURCES = ["hq_block.hip", "hq_block_gemm.hip", "hq_block_gemv.hip", "hq_adamw.hip",
                  "hq_train_api.cpp"]
+# the operators of include/hq_mx.h, likewise
+MX_LIB = os.path.join(HERE, "libhq_mx.so")
+MX_SOURCES = ["hq_mx.hip", "hq_mx_gemm.hip", "hq_mx_gemv.hip", "hq_kv.hip", "hq_kv_attention.hip",
+              "hq_mx_api.cpp"]
 
 # -packed-fp32-ops: hipcc forms packed fp32 ops from plain float code; keep them out.
 HIP_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
@@ -38,7 +42,7 @@ def link(lib, objs, verbose=False, extra=()):
 def build(verbose=False, jobs=None):
     objs = []
     procs = []
-    for src in SOURCES + TRAIN_SOURCES:
+    for src in SOURCES + TRAIN_SOURCES + MX_SOURCES:
         obj = os.path.join(CSRC, src + ".o")
         lang = ["-x", "hip"] if src.endswith(".hip") else []
         cmd = ["hipcc"] + HIP_FLAGS + lang + ["-c", os.path.join(CSRC, src), "-o", obj]
@@ -49,9 +53,10 @@ def build(verbose=False, jobs=None):
     for cmd, p in procs:
         if p.wait() != 0:
             raise RuntimeError("compile failed: " + " ".join(cmd))
-    n = len(SOURCES)
+    n, m = len(SOURCES), len(SOURCES) + len(TRAIN_SOURCES)
     link(LIB, objs[:n], verbose)
-    link(TRAIN_LIB, objs[n:], verbose, TRAIN_LINK)
+    link(TRAIN_LIB, objs[n:m], verbose, TRAIN_LINK)
+    link(MX_LIB, objs[m:], verbose, TRAIN_LINK)
     for o in objs:
         os.remove(o)
     return LIB

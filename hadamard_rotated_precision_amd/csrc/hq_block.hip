@@ -40,59 +40,6 @@ struct BlockQuantArgs {
   int pow2;
 };
 
-// A thread's 8 x 8 elements as they were loaded: 16-bit ones stay packed (32 registers instead of
-// 64, so four workgroups fit a compute unit instead of two) and are widened at each use.
-template <class T, bool WIDE = T::bytes == 4>
-struct Tile8 {
-  float d[8][8];
-  __device__ void load(int i, const void* src, int64_t at, int n) { load8<T>(src, at, n, d[i]); }
-  __device__ float value(int i, int j) const { return d[i][j]; }
-  // largest magnitudes of the rows, and of the columns in pairs (2 q, 2 q + 1), as bit patterns
-  __device__ uint32_t row_mag(int i) const { return mag8(d[i]); }
-  __device__ uint32_t col_mag(int j) const {
-    uint32_t a = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) a = max(a, mag(d[i][j]));
-    return a;
-  }
-  __device__ static uint32_t widen(uint32_t m) { return m; }
-};
-
-template <class T>
-struct Tile8<T, false> {
-  typedef unsigned short us2 __attribute__((ext_vector_type(2)));
-  uint32_t d[8][4];
-  __device__ void load(int i, const void* src, int64_t at, int n) {
-    const uint16_t* p = static_cast<const uint16_t*>(src) + at;
-    if (n >= 8) {
-      __builtin_memcpy(d[i], p, 16);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        d[i][j] = (2 * j < n ? p[2 * j] : 0u) | (2 * j + 1 < n ? static_cast<uint32_t>(p[2 * j + 1]) << 16 : 0u);
-    }
-  }
-  __device__ float value(int i, int j) const {
-    const uint32_t w = d[i][j >> 1];
-    if constexpr (T::is_bf16) return __uint_as_float((j & 1) ? w & 0xFFFF0000u : w << 16);
-    else return T::from_bits(static_cast<uint16_t>((j & 1) ? w >> 16 : w & 0xFFFFu));
-  }
-  __device__ static us2 pair(uint32_t w) { return __builtin_bit_cast(us2, w & 0x7FFF7FFFu); }
-  __device__ uint32_t row_mag(int i) const {
-    const us2 a = __builtin_elementwise_max(__builtin_elementwise_max(pair(d[i][0]), pair(d[i][1])),
-                                            __builtin_elementwise_max(pair(d[i][2]), pair(d[i][3])));
-    return max(static_cast<uint32_t>(a[0]), static_cast<uint32_t>(a[1]));
-  }
-  __device__ uint32_t col_mag(int j) const {
-    us2 a = pair(d[0][j >> 1]);
-#pragma unroll
-    for (int i = 1; i < 8; ++i) a = __builtin_elementwise_max(a, pair(d[i][j >> 1]));
-    return a[j & 1];
-  }
-  // a 16-bit magnitude as the bit pattern of its fp32 value (infinities and NaN stay such)
-  __device__ static uint32_t widen(uint32_t m) { return __float_as_uint(T::from_bits(static_cast<uint16_t>(m))); }
-};
-
 // Lane l of each 16 gets the largest of the sixteen lanes' m[l % 8]: each step halves the values a
 // lane still carries, so 8 x 16 maxima take 8 exchanges instead of 32.
 __device__ inline uint32_t max16_of8(const uint32_t (&m)[8], int lane) {

@@ -1,0 +1,56 @@
+// hq_kv_index.hpp — where a token of a paged cache lies, with the checks that keep a wrong slot,
+// page or length inside the buffers. Plain arithmetic, for the kernels and for tests on the host.
+#pragma once
+
+#include <stdint.h>
+
+#if defined(__HIP__) || defined(__HIPCC__)
+#define HQ_BOTH __host__ __device__ inline
+#else
+#define HQ_BOTH inline
+#endif
+
+namespace hq {
+
+// Row of a slot in k_codes' pages x heads x page rows, or -1 for a slot outside the cache. page is
+// 2^shift.
+HQ_BOTH int64_t kv_row_of_slot(int64_t slot, int64_t pages, int shift, int heads, int head) {
+  if (slot < 0 || slot >= (pages << shift)) return -1;
+  return ((((slot >> shift) * heads) + head) << shift) + (slot & ((int64_t{1} << shift) - 1));
+}
+
+// Row of a sequence's token `at`, whose page is the entry at >> shift of the sequence's table, or -1
+// where the table ends before it or names no page of the cache.
+HQ_BOTH int64_t kv_row_of_token(int at, const int32_t* table, int64_t table_ld, int64_t pages, int shift, int heads,
+                                int head) {
+  const int64_t p = at >> shift;
+  if (at < 0 || p >= table_ld) return -1;
+  const int64_t page = table[p];
+  if (page < 0 || page >= pages) return -1;
+  return (((page * heads) + head) << shift) + (at & ((int64_t{1} << shift) - 1));
+}
+
+// A sequence's query rows [first, first + n) of the tensor's `tokens`, at most max_q of them, and its
+// length, at most max_len. `behind`: new tokens that lie beyond the bounds count as seen by nobody,
+// but row i keeps its position len - (end - first) + i.
+struct KvSequence {
+  int64_t first;
+  int n;          // rows to compute
+  int64_t pos0;   // position of row 0
+  int len;        // tokens that may be seen
+};
+HQ_BOTH KvSequence kv_sequence(int32_t start, int32_t end, int32_t len, int64_t tokens, int max_q, int max_len) {
+  KvSequence s;
+  s.first = start;
+  const int64_t all = static_cast<int64_t>(end) - start;
+  const bool ok = start >= 0 && all > 0;
+  int64_t n = ok ? all : 0;
+  if (ok && s.first + n > tokens) n = tokens > s.first ? tokens - s.first : 0;
+  s.n = static_cast<int>(n < max_q ? n : max_q);
+  const int64_t l = len > 0 ? len : 0;
+  s.pos0 = l - (ok ? all : 0);
+  s.len = static_cast<int>(l < max_len ? l : max_len);
+  return s;
+}
+
+}  // namespace hq

@@ -7,6 +7,7 @@
 
 #include <cmath>
 
+#include "hq_checks.hpp"
 #include "hq_train_internal.hpp"
 
 namespace {
@@ -15,44 +16,17 @@ using hq::BlockGemmPass;
 using hq::BlockOperand;
 using hq::BlockQuantPass;
 
-int64_t pitch16(int64_t n) { return (n + 15) / 16 * 16; }
+using hq::align256;
+using hq::aligned;
+using hq::check_ws;
+using hq::dims_ok;
+using hq::element_aligned;
+using hq::kMaxDim;
+using hq::pitch16;
+using hq::stream_ok;
+using hq::valid_dt;
+
 int64_t blocks(int64_t n) { return (n + HQ_BLOCK - 1) / HQ_BLOCK; }
-size_t align256(size_t n) { return (n + 255) / 256 * 256; }
-bool aligned(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-bool valid_dt(int32_t dt) { return dt == HQ_F32 || dt == HQ_F16 || dt == HQ_BF16; }
-// matrices and vectors of floating-point elements may start at any element
-bool element_aligned(const void* p, int32_t dt) { return aligned(p, dt == HQ_F32 ? 4 : 2); }
-
-// Largest extent of a matrix axis, and 2^38 elements in all: tiles are addressed with 32-bit
-// offsets inside a row block, and workgroup counts stay inside a grid.
-constexpr int64_t kMaxDim = int64_t{1} << 22;
-
-bool dims_ok(int64_t a, int64_t b) {
-  return a >= 0 && b >= 0 && a <= kMaxDim && b <= kMaxDim &&
-         blocks(a) * blocks(b) <= (int64_t{1} << 24);
-}
-
-#define HQ_CHECK(expr)             \
-  do {                             \
-    hq_status s_ = (expr);         \
-    if (s_ != HQ_OK) return s_;    \
-  } while (0)
-#define HQ_TRY(expr)                                  \
-  do {                                                \
-    if ((expr) != hipSuccess) return HQ_ERR_LAUNCH;   \
-  } while (0)
-
-// The library's device checks, and the stream's device: a kernel must not be launched on a
-// stream of another device than the current one.
-hq_status stream_ok(void* stream) {
-  HQ_CHECK(hq::device_ready());
-  if (!stream) return HQ_OK;
-  int cur = 0;
-  hipDevice_t of = 0;
-  if (hipGetDevice(&cur) != hipSuccess) return HQ_ERR_DEVICE;
-  if (hipStreamGetDevice(static_cast<hipStream_t>(stream), &of) != hipSuccess) return HQ_ERR_DEVICE;
-  return of == cur ? HQ_OK : HQ_ERR_DEVICE;
-}
 
 // Buffers of a tensor that a call writes: layouts it asks for, pitches and alignment.
 hq_status check_out(const hq_block_tensor* q, int64_t rows, int64_t cols, int32_t shape,
@@ -158,12 +132,6 @@ hq_block_tensor scratch_tensor(void* ws, int64_t rows, int64_t cols) {
                                       align256(static_cast<size_t>(rows * q.ld)));
   q.lds = rows;
   return q;
-}
-
-hq_status check_ws(const void* ws, size_t have, size_t need) {
-  if (need == 0) return HQ_OK;
-  if (!ws || have < need) return HQ_ERR_WORKSPACE;
-  return aligned(ws, 16) ? HQ_OK : HQ_ERR_ALIGN;
 }
 
 // The product of a validated call.

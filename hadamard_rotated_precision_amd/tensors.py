@@ -577,3 +577,308 @@ class AdamW:
                 "hq_adamw_step")
         if not captured:
             self.step_count += 1
+
+
+# ------------------------------------------------------------------ microscaled 4-bit
+def _mx_blocks(n):
+    return (n + B.HQ_MX_BLOCK - 1) // B.HQ_MX_BLOCK
+
+
+def _seed_ptr(seed, device):
+    """The address of a rounding's seed, a device tensor of one 32-bit integer, or None."""
+    if seed is None:
+        return None
+    if seed.dtype not in (torch.int32, torch.uint32) or seed.numel() != 1 or seed.device != device:
+        raise ValueError("a seed must be one 32-bit integer on %s" % device)
+    return seed.data_ptr()
+
+
+def _workspace(ws, size, device, stream):
+    """The caller's workspace, or one of `size` bytes from the memory of the stream that uses it."""
+    if ws is None:
+        with torch.cuda.stream(stream):
+            return torch.empty(max(size, 16), dtype=torch.uint8, device=device)
+    if ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != device:
+        raise ValueError("ws must be a contiguous uint8 tensor on %s" % device)
+    return ws
+
+
+class MxTensor:
+    """Caller-owned storage of a microscaled 4-bit matrix (hq_mx_tensor): E2M1 codes, two a byte
+    (rows x pitch), their scale bytes (rows x pitch, one for 32 codes), and the same of the transpose
+    (codes_t, scales_t: cols x pitch). rot: 1, or 32 for values rotated by H_32 block by block. New
+    values go into the buffers; the buffers themselves stay, for the library's struct holds their
+    addresses."""
+
+    codes = property(operator.attrgetter("_codes"))
+    codes_t = property(operator.attrgetter("_codes_t"))
+    scales = property(operator.attrgetter("_scales"))
+    scales_t = property(operator.attrgetter("_scales_t"))
+
+    def __init__(self, rows, cols, rot=B.HQ_MX_BLOCK, codes=True, codes_t=True, device="cuda"):
+        if not (codes or codes_t):
+            raise ValueError("an MxTensor holds codes, codes_t or both")
+
+        def new(wanted, n, width):
+            return torch.empty((n, width), dtype=torch.uint8, device=device) if wanted else None
+
+        cb, rb = _mx_blocks(cols), _mx_blocks(rows)
+        self._set(rows, cols, rot, new(codes, rows, 16 * cb), new(codes_t, cols, 16 * rb),
+                  new(codes, rows, pitch16(cb)), new(codes_t, cols, pitch16(rb)))
+
+    def _set(self, rows, cols, rot, codes, codes_t, scales, scales_t):
+        if rot not in (1, B.HQ_MX_BLOCK):
+            raise ValueError("rot is 1 or %d" % B.HQ_MX_BLOCK)
+        self.rows, self.cols, self.rot = rows, cols, rot
+        self._codes, self._codes_t, self._scales, self._scales_t = codes, codes_t, scales, scales_t
+        self.device = (codes if codes is not None else codes_t).device
+        st = self.st = B.hq_mx_tensor()
+        st.codes, st.codes_t = ptr(codes), ptr(codes_t)
+        st.scales, st.scales_t = ptr(scales), ptr(scales_t)
+        st.rows, st.cols, st.rot = rows, cols, rot
+        st.ld, st.ld_t, st.lds, st.lds_t = (BlockTensor._pitch(t)
+                                            for t in (codes, codes_t, scales, scales_t))
+
+    @classmethod
+    def wrap(cls, codes, scales, rows, cols, rot=B.HQ_MX_BLOCK, codes_t=None, scales_t=None):
+        """A matrix whose codes exist already (weights of a checkpoint). The buffers are used as they
+        are: codes at least rows x 16 ceil(cols / 32) bytes, scales at least rows x the multiple of 16
+        from ceil(cols / 32) on. Checks their shapes and, once, on the host, that scale bytes past the
+        last block (and, without rotation, codes past the last column) are zero."""
+        if codes is None or (codes_t is None) != (scales_t is None):
+            raise ValueError("codes are needed, and scales with them")
+        for name, c, s, n, length in (("", codes, scales, rows, cols), ("_t", codes_t, scales_t, cols, rows)):
+            if c is None:
+                continue
+            nb = _mx_blocks(length)
+            for what, t, width in (("codes", c, 16 * nb), ("scales", s, pitch16(nb))):
+                if t.dtype != torch.uint8 or t.dim() != 2 or t.shape[0] != n or t.shape[1] < width:
+                    raise ValueError("%s%s must be a uint8 tensor of at least %d x %d" % (what, name, n, width))
+                if t.stride(1) != 1 and t.shape[1] > 1:
+                    raise ValueError("%s%s must have contiguous rows" % (what, name))
+                if t.device != codes.device:
+                    raise ValueError("%s%s is on %s, not on %s" % (what, name, t.device, codes.device))
+            if n and length:
+                loose = bool(s[:, nb:pitch16(nb)].any())
+                if rot == 1:
+                    loose |= bool(c[:, (length + 1) // 2:16 * nb].any())
+                    loose |= bool(length % 2 and (c[:, length // 2] >> 4).any())
+                if loose:
+                    raise ValueError("codes%s and scales%s must be zero past their ends" % (name, name))
+        self = cls.__new__(cls)
+        self._set(rows, cols, rot, codes, codes_t, scales, scales_t)
+        return self
+
+    def quantize(self, src, seed=None, stream=None):
+        """hq_mx_quantize of src (rows x cols, contiguous) into these buffers. seed: None for
+        rounding to nearest, or a device tensor of one 32-bit integer for rounding at random."""
+        _check_matrix(src, self.rows, self.cols, "src", self.device)
+        B.check(_launch(B.hq_mx_quantize, src, stream, src.data_ptr(), HQ_DT[src.dtype], self.rows,
+                        self.cols, self.rot, _seed_ptr(seed, self.device), self.st), "hq_mx_quantize")
+        return self
+
+    def dequantize(self, dst, side=B.HQ_SIDE_ROWS, stream=None):
+        """hq_mx_dequantize: what the codes (HQ_SIDE_COLS: the transposed ones) stand for, into dst
+        (rows x cols, or cols x rows)."""
+        shape = (self.rows, self.cols) if side == B.HQ_SIDE_ROWS else (self.cols, self.rows)
+        _check_matrix(dst, *shape, "dst", self.device)
+        B.check(_launch(B.hq_mx_dequantize, dst, stream, self.st, side, dst.data_ptr(),
+                        HQ_DT[dst.dtype]), "hq_mx_dequantize")
+        return dst
+
+
+def mx_gemm(a, b, c, a_side=B.HQ_SIDE_ROWS, b_side=B.HQ_SIDE_ROWS, accumulate=False, ws=None,
+            stream=None):
+    """hq_mx_gemm: c (+)= a b^T over MxTensors (HQ_SIDE_COLS reads the transposed codes). ws: a uint8
+    tensor of hq_mx_gemm_workspace_bytes, allocated here when missing."""
+    M, K = (a.rows, a.cols) if a_side == B.HQ_SIDE_ROWS else (a.cols, a.rows)
+    N = b.rows if b_side == B.HQ_SIDE_ROWS else b.cols
+    _check_matrix(c, M, N, "c", a.device)
+    if b.device != a.device:
+        raise ValueError("b is on %s, not on %s" % (b.device, a.device))
+    ws = _workspace(ws, B.hq_mx_gemm_workspace_bytes(M, N, K) if ws is None else 0, a.device, stream)
+    B.check(_launch(B.hq_mx_gemm, c, stream, a.st, a_side, b.st, b_side, c.data_ptr(),
+                    HQ_DT[c.dtype], int(accumulate), ws.data_ptr(), ws.numel()), "hq_mx_gemm")
+
+
+class MxLayer:
+    """Buffers for one linear layer (N tokens, C in, D out) in microscaled 4-bit floating point and
+    its calls, as BlockLayer's.
+
+    train=True keeps Q(X) and Q(dY) in both layouts for the weight gradient; train=False is the
+    serving form (forward alone, nothing saved). weight: an MxTensor that the layer reads (D x C, for
+    instance MxTensor.wrap of a checkpoint's codes), whose rotation the layer takes; without it
+    set_weight quantizes W into codes of the layer's own. seed: of a rounding at random (a device
+    tensor of one 32-bit integer), None for rounding to nearest."""
+
+    def __init__(self, N, C, D, rot=B.HQ_MX_BLOCK, weight=None, train=True, device="cuda"):
+        self.N, self.C, self.D, self.train = N, C, D, train
+        if weight is not None and (weight.rows, weight.cols) != (D, C):
+            raise ValueError("weight is %d x %d, not %d x %d" % (weight.rows, weight.cols, D, C))
+        self.qw = weight or MxTensor(D, C, rot=rot, codes_t=train, device=device)
+        self.rot, self.device = self.qw.rot, self.qw.device
+        self.qx = MxTensor(N, C, rot=self.rot, device=self.device) if train else None
+        self.qg = MxTensor(N, D, rot=self.rot, device=self.device) if train else None
+        self.ws_bytes = B.hq_mx_workspace_bytes(N, C, D)
+        self.ws = torch.empty(max(self.ws_bytes, 16), dtype=torch.uint8, device=self.device)
+
+    def set_weight(self, w, seed=None, stream=None):
+        self.qw.quantize(w, seed, stream)
+
+    def fwd(self, x, y, seed=None, stream=None):
+        _check_matrix(x, self.N, self.C, "x", self.device)
+        _check_matrix(y, self.N, self.D, "y", self.device)
+        B.check(_launch(B.hq_mx_linear_fwd, x, stream, x.data_ptr(), HQ_DT[x.dtype], self.N, self.C,
+                        self.D, self.qw.st, _seed_ptr(seed, self.device), y.data_ptr(),
+                        HQ_DT[y.dtype], None if self.qx is None else self.qx.st, self.ws.data_ptr(),
+                        self.ws_bytes), "hq_mx_linear_fwd")
+
+    def bwd_input(self, dy, dx, seed=None, stream=None):
+        _check_matrix(dy, self.N, self.D, "dy", self.device)
+        _check_matrix(dx, self.N, self.C, "dx", self.device)
+        B.check(_launch(B.hq_mx_linear_bwd_input, dy, stream, dy.data_ptr(), HQ_DT[dy.dtype], self.N,
+                        self.C, self.D, self.qw.st, _seed_ptr(seed, self.device), dx.data_ptr(),
+                        HQ_DT[dx.dtype], None if self.qg is None else self.qg.st, self.ws.data_ptr(),
+                        self.ws_bytes), "hq_mx_linear_bwd_input")
+
+    def bwd_weight(self, dw, accumulate=False, stream=None):
+        """From the codes that fwd and bwd_input saved."""
+        if not self.train:
+            raise ValueError("a layer made with train=False saves nothing for the weight gradient")
+        _check_matrix(dw, self.D, self.C, "dw", self.device)
+        B.check(_launch(B.hq_mx_linear_bwd_weight, dw, stream, self.qg.st, self.qx.st, self.N, self.C,
+                        self.D, dw.data_ptr(), HQ_DT[dw.dtype], int(accumulate), self.ws.data_ptr(),
+                        self.ws_bytes), "hq_mx_linear_bwd_weight")
+
+
+def _check_heads(t, tokens, heads, dim, name, device):
+    """tokens x heads x dim with contiguous elements of a head (a view of a larger projection will
+    do). Returns the strides of tokens and heads."""
+    if tuple(t.shape) != (tokens, heads, dim):
+        raise ValueError("%s has shape %s, not %s" % (name, tuple(t.shape), (tokens, heads, dim)))
+    if t.dtype not in HQ_DT:
+        raise ValueError("%s has dtype %s: fp32, fp16 or bf16 is needed" % (name, t.dtype))
+    if t.stride(2) != 1:
+        raise ValueError("the elements of a head of %s must be contiguous" % name)
+    if t.device != device:
+        raise ValueError("%s is on %s, not on %s" % (name, t.device, device))
+    return t.stride(0), t.stride(1)
+
+
+def _check_index(t, shape, dtype, name, device):
+    if tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous() or t.device != device:
+        raise ValueError("%s must be a contiguous %s tensor of %s on %s" % (name, dtype, shape, device))
+
+
+class KVCache:
+    """Keys and values of a model layer's past in microscaled 4-bit pages (hq_kv_cache): codes
+    (pages x heads x page x head_dim / 2) and scale bytes (pages x heads x page x head_dim / 32) of
+    each. rotate: keep them rotated by H_head_dim, which spreads outlier channels over the blocks.
+    A slot is page_index * page + row."""
+
+    def __init__(self, pages, page, heads, head_dim, rotate=True, device="cuda"):
+        def new(width):
+            return torch.zeros((pages, heads, page, width), dtype=torch.uint8, device=device)
+
+        self._set(new(head_dim // 2), new(head_dim // 32), new(head_dim // 2), new(head_dim // 32), rotate)
+
+    @classmethod
+    def wrap(cls, k_codes, k_scales, v_codes, v_scales, rotate=True):
+        """A cache over buffers of the caller's own, used as they are."""
+        if k_codes.dim() != 4:
+            raise ValueError("codes must be pages x heads x page x head_dim / 2")
+        pages, heads, page, half = k_codes.shape
+        for name, t, width in (("k_codes", k_codes, half), ("k_scales", k_scales, half // 16),
+                               ("v_codes", v_codes, half), ("v_scales", v_scales, half // 16)):
+            _check_index(t, (pages, heads, page, width), torch.uint8, name, k_codes.device)
+        self = cls.__new__(cls)
+        self._set(k_codes, k_scales, v_codes, v_scales, rotate)
+        return self
+
+    def _set(self, k_codes, k_scales, v_codes, v_scales, rotate):
+        self.pages, self.heads, self.page, half = k_codes.shape
+        self.head_dim, self.device = 2 * half, k_codes.device
+        if self.head_dim not in (64, 128, 256):
+            raise ValueError("head_dim is 64, 128 or 256, not %d" % self.head_dim)
+        if self.page & (self.page - 1) or not 16 <= self.page <= 1 << 20:
+            raise ValueError("page is a power of two from 16 to 2^20, not %d" % self.page)
+        self._buffers = (k_codes, k_scales, v_codes, v_scales)    # kept: st holds their addresses
+        st = self.st = B.hq_kv_cache()
+        st.k_codes, st.k_scales, st.v_codes, st.v_scales = map(ptr, self._buffers)
+        st.pages, st.page, st.heads, st.head_dim = self.pages, self.page, self.heads, self.head_dim
+        st.rot = self.head_dim if rotate else 1
+
+    k_codes = property(lambda self: self._buffers[0])
+    k_scales = property(lambda self: self._buffers[1])
+    v_codes = property(lambda self: self._buffers[2])
+    v_scales = property(lambda self: self._buffers[3])
+
+    def append(self, k, v, slots, stream=None):
+        """hq_kv_append: k and v (tokens x heads x head_dim, any strides of tokens and heads) to the
+        slots (int64); a token with a slot outside the cache is left out."""
+        n = slots.numel()
+        _check_index(slots, (n,), torch.int64, "slots", self.device)
+        ks = _check_heads(k, n, self.heads, self.head_dim, "k", self.device)
+        vs = _check_heads(v, n, self.heads, self.head_dim, "v", self.device)
+        if k.dtype != v.dtype:
+            raise ValueError("k and v have dtypes %s and %s" % (k.dtype, v.dtype))
+        B.check(_launch(B.hq_kv_append, k, stream, k.data_ptr(), v.data_ptr(), HQ_DT[k.dtype], n, *ks,
+                        *vs, slots.data_ptr(), self.st), "hq_kv_append")
+
+    def read(self, slots, k=None, v=None, stream=None):
+        """hq_kv_read: keys and/or values of the slots into k and v (n x heads x head_dim, contiguous,
+        one dtype); zeros for slots outside the cache."""
+        n = slots.numel()
+        _check_index(slots, (n,), torch.int64, "slots", self.device)
+        given = [(name, t) for name, t in (("k", k), ("v", v)) if t is not None]
+        if not given:
+            raise ValueError("k, v or both are needed")
+        for name, t in given:
+            _check_heads(t, n, self.heads, self.head_dim, name, self.device)
+            if not t.is_contiguous() or t.dtype != given[0][1].dtype:
+                raise ValueError("k and v must be contiguous and of one dtype")
+        t = given[0][1]
+        B.check(_launch(B.hq_kv_read, t, stream, self.st, slots.data_ptr(), n, ptr(k), ptr(v),
+                        HQ_DT[t.dtype]), "hq_kv_read")
+
+    @staticmethod
+    def _batch(seqs, q_heads, max_q, max_len, window=0, scale=1.0):
+        b = B.hq_kv_batch()
+        b.seqs, b.q_heads, b.max_q, b.max_len, b.window, b.scale = seqs, q_heads, max_q, max_len, window, scale
+        return b
+
+    def attention_workspace(self, seqs, q_heads, max_q, max_len):
+        """A workspace for attend() with these bounds."""
+        size = B.hq_kv_attention_workspace_bytes(self.st, self._batch(seqs, q_heads, max_q, max_len))
+        return torch.empty(max(size, 16), dtype=torch.uint8, device=self.device)
+
+    def attend(self, q, out, q_starts, lens, table, max_q, max_len, scale=None, window=0, lse=None,
+               ws=None, stream=None):
+        """hq_kv_attention of q (tokens x q_heads x head_dim, any strides of tokens and heads) into out
+        (the same shape, contiguous): sequence s has the query rows q_starts[s] .. q_starts[s + 1] and
+        lens[s] tokens in the cache, whose pages table[s] names (all int32). max_q and max_len bound
+        both. scale: 1 / sqrt(head_dim) without it. window: tokens that a query sees, 0 for all.
+        lse: an fp32 tensor (tokens x q_heads), or None. ws: attention_workspace, allocated here when
+        missing."""
+        if q.dim() != 3:
+            raise ValueError("q must be tokens x heads x head_dim")
+        tokens, q_heads, dev = q.shape[0], q.shape[1], self.device
+        strides = _check_heads(q, tokens, q_heads, self.head_dim, "q", dev)
+        _check_heads(out, tokens, q_heads, self.head_dim, "out", dev)
+        if not out.is_contiguous():
+            raise ValueError("out must be contiguous")
+        seqs = lens.numel()
+        _check_index(lens, (seqs,), torch.int32, "lens", dev)
+        _check_index(q_starts, (seqs + 1,), torch.int32, "q_starts", dev)
+        if table.dim() != 2:
+            raise ValueError("table must be sequences x pages")
+        _check_index(table, (seqs, table.shape[1]), torch.int32, "table", dev)
+        if lse is not None:
+            _check_index(lse, (tokens, q_heads), torch.float32, "lse", dev)
+        b = self._batch(seqs, q_heads, max_q, max_len, window,
+                        self.head_dim ** -0.5 if scale is None else scale)
+        b.q_starts, b.lens, b.table, b.table_ld = ptr(q_starts), ptr(lens), ptr(table), table.shape[1]
+        ws = _workspace(ws, B.hq_kv_attention_workspace_bytes(self.st, b) if ws is None else 0, dev, stream)
+        B.check(_launch(B.hq_kv_attention, q, stream, q.data_ptr(), HQ_DT[q.dtype], tokens, *strides,
+                        self.st, b, out.data_ptr(), HQ_DT[out.dtype], ptr(lse), ws.data_ptr(),
+                        ws.numel()), "hq_kv_attention")
