@@ -19,15 +19,20 @@ HQ_BOTH int64_t kv_row_of_slot(int64_t slot, int64_t pages, int shift, int heads
   return ((((slot >> shift) * heads) + head) << shift) + (slot & ((int64_t{1} << shift) - 1));
 }
 
-// Row of a sequence's token `at`, whose page is the entry at >> shift of the sequence's table, or -1
-// where the table ends before it or names no page of the cache.
+// The entry of a sequence's table that names the page of its token `at`, or -1 where the table ends before.
+HQ_BOTH int64_t kv_entry_of_token(int at, int64_t table_ld, int shift) {
+  const int64_t p = at >> shift;
+  return at < 0 || p >= table_ld ? -1 : p;
+}
+// Row of token `at` in the page that the entry names, or -1 where that is no page of the cache.
+HQ_BOTH int64_t kv_row_in_page(int at, int32_t page, int64_t pages, int shift, int heads, int head) {
+  if (page < 0 || page >= pages) return -1;
+  return (((static_cast<int64_t>(page) * heads) + head) << shift) + (at & ((int64_t{1} << shift) - 1));
+}
 HQ_BOTH int64_t kv_row_of_token(int at, const int32_t* table, int64_t table_ld, int64_t pages, int shift, int heads,
                                 int head) {
-  const int64_t p = at >> shift;
-  if (at < 0 || p >= table_ld) return -1;
-  const int64_t page = table[p];
-  if (page < 0 || page >= pages) return -1;
-  return (((page * heads) + head) << shift) + (at & ((int64_t{1} << shift) - 1));
+  const int64_t p = kv_entry_of_token(at, table_ld, shift);
+  return p < 0 ? -1 : kv_row_in_page(at, table[p], pages, shift, heads, head);
 }
 
 // A sequence's query rows [first, first + n) of the tensor's `tokens`, at most max_q of them, and its

@@ -281,7 +281,10 @@ def test_values_that_are_not_numbers():
         for scales in (cache.k_scales, cache.v_scales):
             for s in (50, 63):      # behind the length
                 scales[table[0, s // 16], 0, s % 16] = 255
-        cache.k_codes[table[0, 3], 0, 2:] = 0x77
+        cache.k_codes[table[0, 3], 0, 2:] = cache.v_codes[table[0, 3], 0, 2:] = 0x77
+        again, _ = run(cache, q, starts, [50], table)
+        assert torch.equal(clean, again)
+        cache.k_scales[table[0, 3], 0, 2:] = cache.v_scales[table[0, 3], 0, 2:] = 254     # times 6: past fp32
         again, _ = run(cache, q, starts, [50], table)
         assert torch.equal(clean, again)
         for scales, blocks in ((cache.k_scales, None), (cache.v_scales, slice(32, 64))):
@@ -296,6 +299,27 @@ def test_values_that_are_not_numbers():
         q[4, 1, 3] = math.nan
         out, _ = run(cache, q, starts, [50], table)
         assert out[4, 1].isnan().all() and out.isnan().sum() == 128
+
+
+def test_what_a_compute_unit_held_before_does_not_matter():
+    """Parts of a chunk whose page does not exist are not loaded: after a call over codes and scales of
+    all ones (NaN) and of the largest numbers, the next one's results are its own."""
+    for D in (64, 128, 256):
+        for byte in (254, 255):
+            dirty = R.new_cache(64, 16, 2, D)
+            for t in (dirty.k_scales, dirty.v_scales):
+                t.fill_(byte)
+            for t in (dirty.k_codes, dirty.v_codes):
+                t.fill_(0x77)
+            every = torch.arange(64, dtype=torch.int32, device=DEV).repeat(40, 1)
+            for n in (1, 3, 20):
+                q = heads_of(gen(n), 40 * n, 8, D, torch.bfloat16, False)
+                run(dirty, q, [n * i for i in range(41)], [1000] * 40, every)
+                cache = R.new_cache(20, 16, 2, D)
+                R.fill(cache, gen(n), 2.0)
+                starts, table = R.batch(gen(n + 1), cache, [n, n, 1], [20, 37, 5])
+                table[1, 1] = -1
+                check(cache, heads_of(gen(n + 2), starts[-1], 8, D, torch.bfloat16, False), starts, [20, 37, 5], table)
 
 
 def test_strided_queries():
