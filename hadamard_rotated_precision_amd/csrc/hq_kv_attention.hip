@@ -19,8 +19,9 @@
 // Rotated caches: (H q) . (H k) = D q . k, and the sum of rotated values is the rotated sum, so queries
 // are rotated in the prologue and outputs in the epilogue.
 //
-// Few rows: the four waves of a workgroup share them and take every fourth chunk each; their sums meet
-// in LDS. Many rows: each wave has rows of its own. Either way the tokens may be split over workgroups.
+// Few rows and many tokens: all chunks of a call form a line, of which each wave takes an even piece; a second
+// kernel joins the parts of rows whose tokens lay in several pieces. Few rows and tokens: the waves of a
+// workgroup share the rows, and their sums meet in LDS. Many rows: each wave has rows of its own.
 //
 // Precision: fp32 statistics, scores and accumulators. Of the largest in its block of 32, a query is
 // kept to 2^-18 (QN = 4) or 2^-28 (6; fp32 in or out). Probabilities are split into PN bf16 numbers:
@@ -62,7 +63,7 @@ struct KvAttnArgs {
   int out_dt;
   float* lse;
   int seqs, tiles, splits, tile_rows;
-  int least;                       // chunks of a workgroup at least; 0: a workgroup takes all of its rows' (no parts)
+  int least;                       // chunks of a wave's piece of the line at least; 0: no line
   float* part;                     // parts of rows' tokens: their sums and statistics
   float* stats;
 };
@@ -106,22 +107,21 @@ struct KvTile {
 };
 
 // The chunks of all rows in a line (sequence by sequence, tile by tile, head by head), cut into even
-// pieces, one for each workgroup. A prefix sum over the sequences' tiles by all threads of a
+// pieces, one for each wave of a call. A prefix sum over the sequences' tiles by all threads of a
 // workgroup; every workgroup of a call comes to the same numbers.
 struct KvLine {
   int64_t total;      // chunks of the batch
-  int64_t piece;      // of a workgroup
-  // The tile that chunk `at` of the line lies in: its index and how many chunks lie before it.
-  int tile;
-  int64_t before;
+  int64_t piece;      // of a wave
+  int tile;           // that this wave's piece begins in (or the wanted one); -1: none
+  int64_t before;     // chunks that lie before this tile
 };
 __device__ inline int tile_chunks(const KvAttnArgs& g, int tile) { return KvTile(g, tile / g.tiles, tile % g.tiles, 0).chunks(g); }
 
-// find(total, piece) names the chunk to look for (or < 0: tile of `wanted`, whose chunks are counted).
-template <class F>
-__device__ inline KvLine kv_line(const KvAttnArgs& g, int groups, int wanted, F find) {
-  __shared__ int64_t sums[kWaves + 1];
-  __shared__ KvLine found;
+// wanted < 0: for the pieces of this workgroup's waves; else for a tile. waves: of the call.
+__device__ inline KvLine kv_line(const KvAttnArgs& g, int waves, int wanted) {
+  __shared__ int64_t sums[kWaves];
+  __shared__ int tile_of[kWaves];
+  __shared__ int64_t before_of[kWaves];
   const int n = g.seqs * g.tiles, t = threadIdx.x, lane = t & 63, w = t >> 6;
   const int strip = (n + 64 * kWaves - 1) / (64 * kWaves);
   int64_t mine = 0;
@@ -134,34 +134,39 @@ __device__ inline KvLine kv_line(const KvAttnArgs& g, int groups, int wanted, F 
     if (lane >= m) up_to += x;
   }
   if (lane == 63) sums[w] = up_to;
+  if (t < kWaves) tile_of[t] = -1;
   __syncthreads();
-  int64_t base = 0, total = 0;
+  int64_t base = 0;
+  KvLine line = {0, 0, -1, 0};
 #pragma unroll
   for (int i = 0; i < kWaves; ++i) {
     if (i < w) base += sums[i];
-    total += sums[i];
+    line.total += sums[i];
   }
-  // whole rounds of the workgroup's waves
-  const int64_t even = (total + groups - 1) / groups, piece = max<int64_t>(g.least, (even + kWaves - 1) / kWaves * kWaves);
-  const int64_t at = find(total, piece);
+  line.piece = max<int64_t>(g.least, (line.total + waves - 1) / waves);
   const int64_t from = base + up_to - mine;
-  const bool here = wanted >= 0 ? wanted >= t * strip && wanted < min(n, (t + 1) * strip) : at >= from && at < from + mine;
-  if (t == 0) found = KvLine{total, piece, -1, 0};
-  __syncthreads();
-  if (here) {
-    int64_t before = from;
-    for (int i = t * strip; i < min(n, (t + 1) * strip); ++i) {
-      const int64_t c = static_cast<int64_t>(tile_chunks(g, i)) * g.heads;
-      if (wanted >= 0 ? i == wanted : at < before + c) {
-        found.tile = i;
-        found.before = before;
-        break;
+#pragma unroll
+  for (int k = 0; k < kWaves; ++k) {
+    const int64_t at = (static_cast<int64_t>(blockIdx.x) * kWaves + k) * line.piece;
+    const bool here = wanted >= 0 ? k == 0 && wanted >= t * strip && wanted < min(n, (t + 1) * strip) : at >= from && at < from + mine;
+    if (here) {
+      int64_t before = from;
+      int i = t * strip;
+      for (; i + 1 < min(n, (t + 1) * strip); ++i) {
+        if (wanted >= 0 && i == wanted) break;
+        const int64_t c = static_cast<int64_t>(tile_chunks(g, i)) * g.heads;
+        if (wanted < 0 && at < before + c) break;
+        before += c;
       }
-      before += c;
+      tile_of[k] = i;
+      before_of[k] = before;
     }
   }
   __syncthreads();
-  return found;
+  const int k = wanted >= 0 ? 0 : w;
+  line.tile = tile_of[k];
+  line.before = line.tile >= 0 ? before_of[k] : 0;
+  return line;
 }
 
 // x as PN bf16 numbers that add up to it, eight at a time.
@@ -418,8 +423,13 @@ __device__ __forceinline__ uint32_t widen2(uint32_t w, uint32_t s) {
   return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, __uint_as_float(s), BYTE));
 }
 
-// TOKENS: the waves share 16 RT rows, split the tokens and have a part of each stage each; else each has
-// 16 RT rows of its own and all read the same chunk, of which each loads a tile.
+// How the waves of a workgroup divide the work:
+//   OWN_ROWS  each has 16 RT rows of its own; all read the same chunk, of which each loads a tile
+//   MERGED    they share 16 RT rows and take every fourth chunk each; their sums meet in LDS
+//   ALONE     each has a piece of the line of chunks for itself
+// MERGED and ALONE have a part of each stage for every wave.
+enum KvMode { OWN_ROWS = 0, MERGED = 1, ALONE = 2 };
+
 template <int D, int RT>
 struct KvShared {
   static constexpr int QP = D + 4;           // floats of a row
@@ -431,7 +441,7 @@ struct KvShared {
 
 // Chunks [begin, end) of a tile's; part < 0: these are all of them and the rows are finished, else their sums
 // go to that part of the workspace.
-template <int D, int RT, int QN, int PN, bool TOKENS>
+template <int D, int RT, int QN, int PN, int MODE>
 __device__ __forceinline__ void attend(const KvAttnArgs& g, const KvTile& tile, int begin, int end, int64_t part_at, const KvShared<D, RT>& sh) {
   constexpr int DT = D / 16;                        // 16-wide tiles of the output; elements a lane reads of a token of V
   using Stage = KvStage<D>;
@@ -445,18 +455,19 @@ __device__ __forceinline__ void attend(const KvAttnArgs& g, const KvTile& tile, 
   asm volatile("" : "+v"(t));        // what follows from it is formed here, not kept over a workgroup's tiles
   const int lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
   const int lr = lane & 15, lg = lane >> 4;
-  const int r0 = TOKENS ? tile.r0 : tile.r0 + w * ROWS;     // of this wave
+  const int r0 = tile.r0 + (MODE == OWN_ROWS ? w * ROWS : 0);     // of this wave
   const KvSequence& s = tile.s;
   const int wg_to = tile.end_token(g);
-  KvPages pages(g, tile, (begin + (TOKENS ? w : 0)) * kChunk);
+  KvPages pages(g, tile, (begin + (MODE == MERGED ? w : 0)) * kChunk);
 
   // One chunk: its loads have landed (and, where the waves share it, everybody's), those of the next go
   // out into the other stage, whose last reads are done.
-  constexpr int STEP = TOKENS ? kWaves : 1;
-  int8_t *const s0 = st0 + (TOKENS ? w * Stage::BYTES : 0), *const s1 = st1 + (TOKENS ? w * Stage::BYTES : 0);
+  constexpr int STEP = MODE == MERGED ? kWaves : 1;
+  const int part_of_stage = MODE == OWN_ROWS ? 0 : w * Stage::BYTES;
+  int8_t *const s0 = st0 + part_of_stage, *const s1 = st1 + part_of_stage;
   int64_t row[4] = {-1, -1, -1, -1}, next[4] = {-1, -1, -1, -1};
   auto issue = [&](const int64_t (&r)[4], int8_t* to) {
-    if (TOKENS && g.shift >= 6) {
+    if (MODE != OWN_ROWS && g.shift >= 6) {
       if (r[0] >= 0) {
         Stage::template load_codes<4>(g.k_codes, r[0], Stage::k_codes(to, 0), lane);
         Stage::template load_codes<4>(g.v_codes, r[0], Stage::v_codes(to, 0), lane);
@@ -467,15 +478,15 @@ __device__ __forceinline__ void attend(const KvAttnArgs& g, const KvTile& tile, 
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if ((TOKENS || i == w) && r[i] >= 0) {
+      if ((MODE != OWN_ROWS || i == w) && r[i] >= 0) {
         Stage::template load_codes<1>(g.k_codes, r[i], Stage::k_codes(to, i), lane);
         Stage::template load_codes<1>(g.v_codes, r[i], Stage::v_codes(to, i), lane);
       }
     }
-    if (TOKENS || w == 0) Stage::load_scales(g.k_scales, r, Stage::k_scales(to), lane);
-    if (TOKENS || w == 1) Stage::load_scales(g.v_scales, r, Stage::v_scales(to), lane);
+    if (MODE != OWN_ROWS || w == 0) Stage::load_scales(g.k_scales, r, Stage::k_scales(to), lane);
+    if (MODE != OWN_ROWS || w == 1) Stage::load_scales(g.v_scales, r, Stage::v_scales(to), lane);
   };
-  int c = begin + (TOKENS ? w : 0);
+  int c = begin + (MODE == MERGED ? w : 0);
   if (c < end) {       // on their way while the queries are prepared
     pages.chunk(c * kChunk, wg_to, row);
     issue(row, s0);
@@ -484,26 +495,34 @@ __device__ __forceinline__ void attend(const KvAttnArgs& g, const KvTile& tile, 
   // queries: rotated in fp32, split into parts
   v6u qp[RT][KU][QI];
   int qb[RT][KU][(QI + 3) / 4] = {};                        // the parts' scale bytes, four to a dword
-  if constexpr (TOKENS) {
-    // eight elements a thread, through the second stage to the lanes of the second operand
-    float* const rows = reinterpret_cast<float*>(st1);
-    for (int e = t; e < ROWS * D / 8; e += 64 * kWaves) {
-      const int r = tile.r0 + e / (D / 8), i = e % (D / 8);
+  // eight elements a lane, through the second stage to the lanes of the second operand; `count` rows from row
+  // `first` of the tile by lanes at, at + step, ..
+  auto bring_rows = [&](float* rows, int first, int count, int at, int by) {
+    for (int e = at; e < count * D / 8; e += by) {
+      const int r = tile.r0 + first + e / (D / 8), i = e % (D / 8);
       float v[8];
       const bool in = r < tile.rows;
       load8_any(g.q, g.q_dt, in ? tile.token(g, r) * g.q_token + tile.q_head(g, r) * g.q_head + 8 * i : 0, in ? 8 : 0, v);
       if (g.rot > 1) rotate_lanes<D>(v, lane);
       float* const to = rows + (e / (D / 8)) * QP + 8 * i;
-      *reinterpret_cast<v4f*>(to) = v4f{v[0], v[1], v[2], v[3]} * g.sign;
-      *reinterpret_cast<v4f*>(to + 4) = v4f{v[4], v[5], v[6], v[7]} * g.sign;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) to[j] = v[j] * g.sign;
     }
+  };
+  if constexpr (MODE == MERGED) {
+    bring_rows(reinterpret_cast<float*>(st1), 0, ROWS, t, 64 * kWaves);
     __syncthreads();
   }
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     float x[KU][32];
-    if constexpr (TOKENS) {
-      const float* const rows = reinterpret_cast<const float*>(st1) + (16 * rt + lr) * QP + 32 * (D == 64 ? lg & 1 : lg);
+    if constexpr (MODE != OWN_ROWS) {
+      if constexpr (MODE == ALONE) {
+        bring_rows(reinterpret_cast<float*>(s1), 16 * rt, 16, lane, 64);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");      // the wave's own writes
+      }
+      const float* const rows = reinterpret_cast<const float*>(MODE == ALONE ? s1 : st1) + ((MODE == ALONE ? 0 : 16 * rt) + lr) * QP +
+                                32 * (D == 64 ? lg & 1 : lg);
 #pragma unroll
       for (int u = 0; u < KU; ++u)
 #pragma unroll
@@ -556,7 +575,8 @@ __device__ __forceinline__ void attend(const KvAttnArgs& g, const KvTile& tile, 
     }
   }
 
-  if constexpr (TOKENS) __syncthreads();       // the second stage is free again
+  // the second stage is free again
+  if constexpr (MODE == MERGED) __syncthreads();
 
   // tokens that this lane's rows see: [from, to); and those of all rows, and of any (of the wave: one whose
   // rows lie behind the last sees nothing)
@@ -724,7 +744,7 @@ __device__ __forceinline__ void attend(const KvAttnArgs& g, const KvTile& tile, 
 
   auto step = [&](int c, int8_t* cur, int8_t* other) {
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-    if constexpr (!TOKENS) __builtin_amdgcn_s_barrier();
+    if constexpr (MODE == OWN_ROWS) __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
     if (c + STEP < end) {
       pages.chunk((c + STEP) * kChunk, wg_to, next);
@@ -732,7 +752,7 @@ __device__ __forceinline__ void attend(const KvAttnArgs& g, const KvTile& tile, 
     }
     __builtin_amdgcn_sched_barrier(0);
     const int t0 = c * kChunk;
-    if (TOKENS || (t0 < any_to && t0 + kChunk > any_from)) {
+    if (MODE != OWN_ROWS || (t0 < any_to && t0 + kChunk > any_from)) {
       const bool ok[4] = {row[0] >= 0, row[1] >= 0, row[2] >= 0, row[3] >= 0};
       compute(!(ok[0] && ok[1] && ok[2] && ok[3]) || t0 + kChunk > all_to || t0 < all_from, cur, ok, t0);
     }
@@ -767,7 +787,7 @@ __device__ __forceinline__ void attend(const KvAttnArgs& g, const KvTile& tile, 
     l[rt] += __shfl_xor(l[rt], 32, 64);
   }
 
-  if constexpr (!TOKENS) {
+  if constexpr (MODE != MERGED) {
     // a lane holds D / 4 consecutive elements of a row, from D / 4 lg on
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
@@ -851,149 +871,172 @@ __device__ __forceinline__ void attend(const KvAttnArgs& g, const KvTile& tile, 
   }
 }
 
-// A workgroup's piece of the line of chunks (TOKENS, least > 0), or one tile's tokens or a split of them.
-template <int D, int RT, int QN, int PN, bool TOKENS>
+template <int D, int RT, int QN, int PN, int MODE>
 __global__ __launch_bounds__(64 * kWaves, 2) void kv_attention_kernel(KvAttnArgs g) {
-  constexpr int PARTS = TOKENS ? kWaves : 1;
+  constexpr int PARTS = MODE == OWN_ROWS ? 1 : kWaves;
   __shared__ __attribute__((aligned(16))) int8_t st0[PARTS * KvStage<D>::BYTES];
   __shared__ __attribute__((aligned(16))) int8_t st1[PARTS * KvStage<D>::BYTES];
-  __shared__ float wave_m[PARTS][16 * RT], wave_l[PARTS][16 * RT];
+  __shared__ float wave_m[MODE == MERGED ? kWaves : 1][16 * RT], wave_l[MODE == MERGED ? kWaves : 1][16 * RT];
   const KvShared<D, RT> sh{st0, st1, wave_m, wave_l};
-  if constexpr (!TOKENS) {
+  if constexpr (MODE != ALONE) {
+    // one tile's tokens, or a split of them
     const int split = static_cast<int>(blockIdx.x % g.splits), work = static_cast<int>(blockIdx.x / g.splits);
     const int at = work % g.tiles, sh_at = work / g.tiles;
     const KvTile tile(g, sh_at / g.heads, at, sh_at % g.heads);
     if (tile.r0 >= tile.rows) return;
     const int first = tile.first_chunk(g), chunks = tile.chunks(g), per = (chunks + g.splits - 1) / g.splits;
-    attend<D, RT, QN, PN, TOKENS>(g, tile, first + min(chunks, split * per), first + min(chunks, (split + 1) * per),
-                                  g.splits > 1 ? static_cast<int64_t>(blockIdx.x) : -1, sh);
+    attend<D, RT, QN, PN, MODE>(g, tile, first + min(chunks, split * per), first + min(chunks, (split + 1) * per),
+                                g.splits > 1 ? static_cast<int64_t>(blockIdx.x) : -1, sh);
   } else {
-    // one loop for both: a piece of several tiles' chunks, or one tile's
-    int at, head, skip;            // tile, head, chunks of it that lie before the piece
-    int left;                      // chunks of the piece
-    if (g.least == 0) {
-      at = static_cast<int>(blockIdx.x / g.heads);
-      head = static_cast<int>(blockIdx.x % g.heads);
-      skip = 0, left = 1;
-    } else {
-      const KvLine line = kv_line(g, gridDim.x, -1, [&](int64_t, int64_t piece) { return blockIdx.x * piece; });
-      if (line.tile < 0) return;
-      left = static_cast<int>(min(line.piece, line.total - blockIdx.x * line.piece));
-      const int64_t off = blockIdx.x * line.piece - line.before;
-      const int n = max(tile_chunks(g, line.tile), 1);
-      at = line.tile;
-      head = static_cast<int>(off / n);
-      skip = static_cast<int>(off % n);
-    }
+    const int wave = static_cast<int>(blockIdx.x) * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const KvLine line = kv_line(g, gridDim.x * kWaves, -1);
     // the same in all lanes: addresses and loops stay scalar
-    at = __builtin_amdgcn_readfirstlane(at);
-    head = __builtin_amdgcn_readfirstlane(head);
-    skip = __builtin_amdgcn_readfirstlane(skip);
-    left = __builtin_amdgcn_readfirstlane(left);
-    while (true) {
+    int at = __builtin_amdgcn_readfirstlane(line.tile);
+    if (at < 0) return;
+    const int64_t start = wave * line.piece, off = start - line.before;
+    const int in_tile = max(tile_chunks(g, at), 1);
+    int left = __builtin_amdgcn_readfirstlane(static_cast<int>(min(line.piece, line.total - start)));   // chunks of the piece
+    int head = __builtin_amdgcn_readfirstlane(static_cast<int>(off / in_tile));
+    int skip = __builtin_amdgcn_readfirstlane(static_cast<int>(off % in_tile));                            // of the tile's, before it
+    while (left > 0 && at < g.seqs * g.tiles) {
       const KvTile tile(g, at / g.tiles, at % g.tiles, head);
-      const int n = tile.chunks(g), first = tile.first_chunk(g);
-      const int take = g.least == 0 ? n : min(left, n - skip);
-      if (tile.r0 < tile.rows && (take > 0 || g.least == 0)) {
-        // a workgroup has two parts: of a tile that it goes on with, and of one that it begins
-        const int64_t part = take == n ? -1 : 2 * static_cast<int64_t>(blockIdx.x) + (skip == 0);
-        attend<D, RT, QN, PN, TOKENS>(g, tile, first + skip, first + skip + take, part, sh);
-      }
+      const int n = tile.chunks(g), first = tile.first_chunk(g), take = min(left, n - skip);
+      // a wave has two parts: of a tile that it goes on with, and of one that it begins
+      if (take > 0)
+        attend<D, RT, QN, PN, MODE>(g, tile, first + skip, first + skip + take, take == n ? -1 : 2 * static_cast<int64_t>(wave) + (skip == 0), sh);
       left -= take;
-      if (g.least == 0 || left <= 0) return;
       skip = 0;
       if (n == 0 || ++head == g.heads) head = 0, ++at;
-      if (at >= g.seqs * g.tiles) return;
-      __syncthreads();             // the stages are free again
     }
   }
 }
 
-// Parts `first`, first + stride, .. (count of them) of a tile's rows, to a common maximum, in their order.
+// The parts of a tile's rows to a common maximum: a wave's lanes hold 512 / D rows, eight elements each;
+// the waves take every fourth part, four in flight, and their sums meet in LDS. Parts: first, then second,
+// second + stride, .. (count of them).
 template <int D>
-__device__ inline void join_parts(const KvAttnArgs& g, const KvTile& tile, int64_t first, int64_t second, int64_t stride, int count) {
-  const int step = g.tile_rows;
-  auto part = [&](int k) { return k == 0 ? first : second + (k - 1) * stride; };
-  for (int e = threadIdx.x; e < step * D / 8; e += 256) {
-    const int r = e / (D / 8), i = e % (D / 8);
-    // whole waves behind the last row have written nothing (and a lane's neighbours are of its row)
-    if (tile.r0 + r >= tile.rows) break;
-    float big = -__builtin_inff();
-#pragma unroll 4
-    for (int k = 0; k < count; ++k) big = fmaxf(big, g.stats[2 * (part(k) * step + r)]);
-    const float base = big == -__builtin_inff() ? 0.0f : big;
-    float total = 0.0f, v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-    for (int k = 0; k < count; ++k) {
-      const int64_t at = part(k) * step + r;
-      const float f = __builtin_amdgcn_exp2f(g.stats[2 * at] - base);
-      total += g.stats[2 * at + 1] * f;
-      float x[8];
-      load8<F32>(g.part, at * D + 8 * i, 8, x);
+__device__ inline void join_parts(const KvAttnArgs& g, const KvTile& tile, int row0, int64_t first, int64_t second, int64_t stride, int count) {
+  constexpr int U = 4;
+  __shared__ float sums[kWaves][64][12];
+  const int t = threadIdx.x, lane = t & 63, w = t >> 6;
+  const int r = row0 + lane / (D / 8), i = lane % (D / 8);
+  const bool in = r < g.tile_rows && tile.r0 + r < tile.rows;      // rows behind the last have no parts
+  float m = -__builtin_inff(), l = 0.0f, v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  for (int k = w; k < count; k += kWaves * U) {
+    float pm[U], pl[U], x[U][8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = __builtin_fmaf(x[j], f, v[j]);
+    for (int u = 0; u < U; ++u) {
+      const int j = k + kWaves * u;
+      pm[u] = -__builtin_inff(), pl[u] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[u][e] = 0.0f;
+      if (in && j < count) {
+        const int64_t at = (j == 0 ? first : second + (j - 1) * stride) * g.tile_rows + r;
+        pm[u] = g.stats[2 * at];
+        pl[u] = g.stats[2 * at + 1];
+        load8<F32>(g.part, at * D + 8 * i, 8, x[u]);
+      }
     }
-    finish_row<D>(g, tile, tile.r0 + r, i, total, base, true, v);
+    float top = m;
+#pragma unroll
+    for (int u = 0; u < U; ++u) top = fmaxf(top, pm[u]);
+    const float base = top == -__builtin_inff() ? 0.0f : top, f = __builtin_amdgcn_exp2f(m - base);
+    l *= f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float h = __builtin_amdgcn_exp2f(pm[u] - base);
+      l = __builtin_fmaf(pl[u], h, l);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(x[u][e], h, v[e]);
+    }
+    m = top;
   }
+  float* const mine = sums[w][lane];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) mine[e] = v[e];
+  mine[8] = m;
+  mine[9] = l;
+  __syncthreads();
+  if (w > 0) return;
+  float big = sums[0][lane][8];
+#pragma unroll
+  for (int k = 1; k < kWaves; ++k) big = fmaxf(big, sums[k][lane][8]);
+  const float base = big == -__builtin_inff() ? 0.0f : big;
+  float total = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+#pragma unroll
+  for (int k = 0; k < kWaves; ++k) {
+    const float f = __builtin_amdgcn_exp2f(sums[k][lane][8] - base);
+    total = __builtin_fmaf(sums[k][lane][9], f, total);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(sums[k][lane][e], f, v[e]);
+  }
+  finish_row<D>(g, tile, tile.r0 + r, i, total, base, in, v);
 }
 
-// The splits' sums (least = 0), or the parts of a tile that lay in several workgroups' pieces of the line; and
-// the rows that see nothing, which lie in none.
+// The splits' sums (least = 0), or the parts of a tile that lay in several waves' pieces of the line; and
+// the rows that see nothing, which lie in none. `groups` workgroups to a tile.
 template <int D>
-__global__ __launch_bounds__(256) void kv_join_kernel(KvAttnArgs g, int groups) {
+__global__ __launch_bounds__(64 * kWaves) void kv_join_kernel(KvAttnArgs g, int waves, int groups) {
+  const int row0 = static_cast<int>(blockIdx.x % groups) * (512 / D), work = static_cast<int>(blockIdx.x / groups);
   if (g.least == 0) {
-    const int work = blockIdx.x, at = work % g.tiles, sh_at = work / g.tiles;
+    const int at = work % g.tiles, sh_at = work / g.tiles;
     const KvTile tile(g, sh_at / g.heads, at, sh_at % g.heads);
-    if (tile.r0 < tile.rows) join_parts<D>(g, tile, static_cast<int64_t>(work) * g.splits, static_cast<int64_t>(work) * g.splits + 1, 1, g.splits);
+    if (tile.r0 + row0 < tile.rows)
+      join_parts<D>(g, tile, row0, static_cast<int64_t>(work) * g.splits, static_cast<int64_t>(work) * g.splits + 1, 1, g.splits);
     return;
   }
-  const int at = blockIdx.x / g.heads, head = blockIdx.x % g.heads;
-  const KvLine line = kv_line(g, groups, at, [](int64_t, int64_t) { return int64_t{-1}; });
+  const int at = work / g.heads, head = work % g.heads;
   const KvTile tile(g, at / g.tiles, at % g.tiles, head);
-  if (tile.r0 >= tile.rows) return;
+  if (tile.r0 + row0 >= tile.rows) return;
+  const KvLine line = kv_line(g, waves, at);
   const int n = tile.chunks(g);
   const int64_t off = line.before + static_cast<int64_t>(head) * n;
   const int64_t w0 = off / line.piece, w1 = (off + max(n, 1) - 1) / line.piece;
-  if (n == 0) join_parts<D>(g, tile, 0, 0, 0, 0);
-  else if (w0 != w1) join_parts<D>(g, tile, 2 * w0 + 1, 2 * (w0 + 1), 2, static_cast<int>(w1 - w0 + 1));
+  if (n == 0) join_parts<D>(g, tile, row0, 0, 0, 0, 0);
+  else if (w0 != w1) join_parts<D>(g, tile, row0, 2 * w0 + 1, 2 * (w0 + 1), 2, static_cast<int>(w1 - w0 + 1));
 }
 
-// How a call is cut up. Rows of a sequence and head: up to 64 (32 with 256 elements) the waves of a workgroup
-// share 32 (16) of them and split the tokens; more: each wave has 32 (16) of its own. Parts of the tokens over
-// workgroups, while the rows alone leave the chip idle: in even pieces of the line of all chunks where the
-// waves share rows, in a fixed number of splits else.
+// How a call is cut up. Rows of a sequence and head: up to 64 (32 with 256 elements) a workgroup or wave takes
+// 32 (16) of them with all their tokens or a part of them; more: each wave of a workgroup has 32 (16) of
+// its own, and the tokens may be split.
 struct KvPlan {
-  bool tokens;        // the waves share the rows
+  int mode;
   int rt;
   int tile_rows;
   int64_t tiles;      // of a sequence and head
   int64_t work;       // of the batch
-  int splits;         // rows of the waves' own
-  int least;          // shared rows: chunks of a piece at least; 0: no pieces
+  int splits;
+  int least;          // ALONE: chunks of a wave's piece at least
   int64_t grid, parts;
 };
 static KvPlan kv_plan(const hq_kv_cache& c, const hq_kv_batch& b) {
   KvPlan p = {};
   const int64_t rows = static_cast<int64_t>(b.max_q) * (b.q_heads / c.heads);
-  p.tokens = rows <= (c.head_dim == 256 ? 32 : 64);
+  const bool few = rows <= (c.head_dim == 256 ? 32 : 64);
+  p.mode = few ? MERGED : OWN_ROWS;
   p.rt = c.head_dim < 256 && rows > 16 ? 2 : 1;
-  p.tile_rows = 16 * p.rt * (p.tokens ? 1 : kWaves);
+  p.tile_rows = 16 * p.rt * (few ? 1 : kWaves);
   p.tiles = (rows + p.tile_rows - 1) / p.tile_rows;
   p.work = static_cast<int64_t>(b.seqs) * c.heads * p.tiles;
   p.splits = 1;
   p.grid = p.work;
   const int64_t chunks = (static_cast<int64_t>(b.max_len) + kChunk - 1) / kChunk + 1;
-  if (p.tokens) {
+  if (few) {
     const int64_t fit = 256 * (c.head_dim == 64 ? 3 : c.head_dim == 128 ? 2 : 1);   // workgroups on the chip
     if (chunks > 4 * kWaves && p.work < 8 * fit) {
-      p.least = 2 * kWaves;
-      const int64_t most = (p.work * chunks + p.least - 1) / p.least;
+      p.mode = ALONE;
+      p.least = 2;
+      const int64_t most = (p.work * chunks + p.least * kWaves - 1) / (p.least * kWaves);
       p.grid = most < fit ? most : fit;
-      p.parts = 2 * p.grid;
+      p.parts = 2 * kWaves * p.grid;
     }
   } else {
     const int64_t most = (chunks + 3) / 4;
-    int64_t s = p.work > 0 ? (1024 + p.work - 1) / p.work : 1;
+    int64_t s = p.work > 0 ? 512 / p.work : 1;      // two workgroups to a compute unit
     s = s < most ? s : most;
     p.splits = static_cast<int>(s < 1 ? 1 : s > 256 ? 256 : s);
     p.grid = p.work * p.splits;
@@ -1010,21 +1053,27 @@ size_t kv_attention_ws(const hq_kv_cache& c, const hq_kv_batch& b) {
   return part_bytes(p, c.head_dim) + static_cast<size_t>(p.parts) * p.tile_rows * 2 * sizeof(float);
 }
 
-template <int D, int RT, bool TOKENS>
+template <int D, int RT, int MODE>
 static hipError_t launch_shape(const KvAttnArgs& a, const KvPlan& p, hipStream_t st, int tok) {
   const dim3 grid(static_cast<unsigned>(p.grid)), block(64 * kWaves);
-  if (a.q_dt == DT_F32 || a.out_dt == DT_F32) return launch_k(kv_attention_kernel<D, RT, 6, 3, TOKENS>, grid, block, st, tok, a);
-  return launch_k(kv_attention_kernel<D, RT, 4, 2, TOKENS>, grid, block, st, tok, a);
+  if (a.q_dt == DT_F32 || a.out_dt == DT_F32) return launch_k(kv_attention_kernel<D, RT, 6, 3, MODE>, grid, block, st, tok, a);
+  return launch_k(kv_attention_kernel<D, RT, 4, 2, MODE>, grid, block, st, tok, a);
+}
+
+template <int D, int RT>
+static hipError_t launch_few(const KvAttnArgs& a, const KvPlan& p, hipStream_t st, int tok) {
+  return p.mode == ALONE ? launch_shape<D, RT, ALONE>(a, p, st, tok) : launch_shape<D, RT, MERGED>(a, p, st, tok);
 }
 
 template <int D>
 static hipError_t launch_dim(const KvAttnArgs& a, const KvPlan& p, hipStream_t st, int tok) {
   constexpr int WIDE = D < 256 ? 2 : 1;
-  const hipError_t e = !p.tokens ? launch_shape<D, WIDE, false>(a, p, st, tok)
-                       : p.rt == 1 ? launch_shape<D, 1, true>(a, p, st, tok) : launch_shape<D, WIDE, true>(a, p, st, tok);
+  const hipError_t e = p.mode == OWN_ROWS ? launch_shape<D, WIDE, OWN_ROWS>(a, p, st, tok)
+                       : p.rt == 1 ? launch_few<D, 1>(a, p, st, tok) : launch_few<D, WIDE>(a, p, st, tok);
   if (e != hipSuccess || p.parts == 0) return e;
-  return launch_k(kv_join_kernel<D>, dim3(static_cast<unsigned>(p.work)), dim3(256), st,
-                  prof_open(K_MISC, static_cast<double>(part_bytes(p, D))), a, static_cast<int>(p.grid));
+  const int groups = (p.tile_rows * D + 511) / 512;
+  return launch_k(kv_join_kernel<D>, dim3(static_cast<unsigned>(p.work * groups)), dim3(64 * kWaves), st,
+                  prof_open(K_MISC, static_cast<double>(part_bytes(p, D))), a, static_cast<int>(p.grid) * kWaves, groups);
 }
 
 hipError_t kv_attention_pass(const KvAttentionPass& p, hipStream_t st) {
