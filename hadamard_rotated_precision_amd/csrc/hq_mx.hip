@@ -66,7 +66,9 @@ __global__ __launch_bounds__(256) void mx_quant_rows_kernel(MxQuantArgs g) {
 // either direction, 8 and 16 across lanes.
 template <class T, int ROT, bool RANDOM>
 __global__ __launch_bounds__(256) void mx_quant_kernel(MxQuantArgs g) {
-  __shared__ __attribute__((aligned(16))) uint8_t turned[128 * 80];   // 64 code bytes a column
+  // 64 code bytes of a row and of a column: a wave's dwords of the eight columns (rows) of a lane spread over
+  // the banks at a pitch of 80
+  __shared__ __attribute__((aligned(16))) uint8_t straight[128 * 80], turned[128 * 80];
   __shared__ __attribute__((aligned(4))) uint8_t rs[128][4], cs[128][4];
   const int t = threadIdx.x, cg = t & 15, rg = t >> 4, wave = t >> 6;
   const int tr = blockIdx.x / g.tiles_c, tc = blockIdx.x % g.tiles_c;
@@ -92,7 +94,7 @@ __global__ __launch_bounds__(256) void mx_quant_kernel(MxQuantArgs g) {
       const int byte = mx_scale_byte(quad_max(mag8(v)));
       const uint32_t key = RANDOM ? mx_row_key(seed, row0 + i) : 0u;
       const uint32_t w = mx_codes8<RANDOM>(v, byte, key, static_cast<uint32_t>(col0 >> 1));
-      if (row0 + i < g.rows && in) *reinterpret_cast<uint32_t*>(g.codes + (row0 + i) * g.ld + (col0 >> 1)) = w;
+      *reinterpret_cast<uint32_t*>(&straight[(8 * rg + i) * 80 + 4 * cg]) = w;
       if ((t & 3) == 0) rs[8 * rg + i][cg >> 2] = in ? byte : 0;
     }
   }
@@ -106,15 +108,15 @@ __global__ __launch_bounds__(256) void mx_quant_kernel(MxQuantArgs g) {
       if constexpr (ROT > 1) {
         fwht_inreg<8, 8>(a);
         fwht_inreg<8, 8>(b);
-        fwht_xlane_c<16>(a, t & 63);
-        fwht_xlane_c<16>(b, t & 63);
-        fwht_xlane_c<32>(a, t & 63);
-        fwht_xlane_c<32>(b, t & 63);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) fwht_swap<16>(a[i], b[i]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) fwht_swap<32>(a[i], b[i]);
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const float (&v)[8] = e ? b : a;
-        const int byte = mx_scale_byte(shfl_max(shfl_max(mag8(v), 16), 32));
+        const int byte = mx_scale_byte(swap_max<32>(swap_max<16>(mag8(v))));
         const uint32_t key = RANDOM ? mx_row_key(seed + 0x9E3779B9u, col0 + j + e) : 0u;
         const uint32_t w = mx_codes8<RANDOM>(v, byte, key, static_cast<uint32_t>(row0 >> 1));
         const int c = 8 * cg + j + e;
@@ -138,35 +140,46 @@ __global__ __launch_bounds__(256) void mx_quant_kernel(MxQuantArgs g) {
     if (r0 + 128 >= g.rows)
       for (int64_t b = 4 * (tr + 1); b < up((g.rows + 31) >> 5, 16); b += 4) *++s = 0;
   }
-  if (!g.codes_t) return;
-  // four lanes cover the 64 bytes of a transposed row
+  // four lanes cover the 64 bytes of a row
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
     const int c = (t >> 2) + 64 * p, part = t & 3;
-    if (c0 + c < g.cols && r0 + 32 * part < g.rows)
+    if (g.codes && r0 + c < g.rows && c0 + 32 * part < g.cols)
+      *reinterpret_cast<uint4*>(g.codes + (r0 + c) * g.ld + (c0 >> 1) + 16 * part) =
+          *reinterpret_cast<const uint4*>(&straight[c * 80 + 16 * part]);
+    if (g.codes_t && c0 + c < g.cols && r0 + 32 * part < g.rows)
       *reinterpret_cast<uint4*>(g.codes_t + (c0 + c) * g.ld_t + (r0 >> 1) + 16 * part) =
           *reinterpret_cast<const uint4*>(&turned[c * 80 + 16 * part]);
   }
 }
 
-// rows x cols values of codes: a thread takes eight of a row, four lanes a block.
-template <class Out, int ROT>
+// rows x cols values of codes: a thread takes eight of each of R rows, four lanes a block.
+template <class Out, int ROT, int R>
 __global__ __launch_bounds__(256) void mx_dequant_kernel(MxOperand q, int64_t rows, int64_t cols, void* dst) {
   const int t = threadIdx.x;
   const int span = static_cast<int>((cols + 2047) >> 11);
-  const int64_t row = blockIdx.x / span;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x / span) * R;
   const int64_t col0 = static_cast<int64_t>(blockIdx.x % span) * 2048 + 8 * t;
   const bool in = col0 < up(cols, 32);
-  const uint32_t w = in ? *reinterpret_cast<const uint32_t*>(q.codes + row * q.ld + (col0 >> 1)) : 0u;
-  const int byte = in ? q.scales[row * q.lds + (col0 >> 5)] : 0;
-  float v[8];
-  mx_values8(w, v);
-  // sums of 32 codes are exact; byte 0 stands for 2^-127, byte 255 for NaN
-  if constexpr (ROT > 1) rotate_lanes<ROT>(v, t);
-  const float s = byte == 255 ? __uint_as_float(0x7FC00000u) : byte ? mx_scale(byte) : 5.87747175e-39f;
+  uint32_t w[R];
+  int byte[R];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = v[j] * (1.0f / ROT) * s;
-  if (col0 < cols) store8<Out>(dst, row * cols + col0, cols - col0, v);
+  for (int i = 0; i < R; ++i) {
+    const int64_t row = min(row0 + i, rows - 1);
+    w[i] = in ? *reinterpret_cast<const uint32_t*>(q.codes + row * q.ld + (col0 >> 1)) : 0u;
+    byte[i] = in ? q.scales[row * q.lds + (col0 >> 5)] : 0;
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    float v[8];
+    mx_values8(w[i], v);
+    // sums of 32 codes are exact; byte 0 stands for 2^-127, byte 255 for NaN
+    if constexpr (ROT > 1) rotate_lanes<ROT>(v, t);
+    const float s = byte[i] == 255 ? __uint_as_float(0x7FC00000u) : byte[i] ? mx_scale(byte[i]) : 5.87747175e-39f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = v[j] * (1.0f / ROT) * s;
+    if (col0 < cols && row0 + i < rows) store8_stream<Out>(dst, (row0 + i) * cols + col0, cols - col0, v);
+  }
 }
 
 template <class T, int ROT, bool RANDOM>
@@ -205,16 +218,20 @@ hipError_t mx_quant_pass(const MxQuantPass& p, hipStream_t st) {
 hipError_t mx_dequant_pass(const MxOperand& q, int64_t rows, int64_t cols, int rot, void* dst, int out_dt, hipStream_t st) {
   const double units = static_cast<double>(rows) * cols * ((out_dt == DT_F32 ? 4 : 2) + 17.0 / 32.0);
   const int tok = prof_open(K_ROT_STORE, units);
-  const dim3 grid(static_cast<unsigned>(rows * ((cols + 2047) / 2048))), block(256);
-#define HQ_D(T)                                                                              \
-  return rot == 1 ? launch_k(mx_dequant_kernel<T, 1>, grid, block, st, tok, q, rows, cols, dst) \
-                  : launch_k(mx_dequant_kernel<T, 32>, grid, block, st, tok, q, rows, cols, dst)
+  const int64_t span = (cols + 2047) / 2048;
+  const bool many = rows * span >= 4096;
+  const dim3 grid(static_cast<unsigned>((many ? (rows + 3) / 4 : rows) * span)), block(256);
+#define HQ_R(T, ROT)                                                                               \
+  (many ? launch_k(mx_dequant_kernel<T, ROT, 4>, grid, block, st, tok, q, rows, cols, dst)         \
+        : launch_k(mx_dequant_kernel<T, ROT, 1>, grid, block, st, tok, q, rows, cols, dst))
+#define HQ_D(T) return rot == 1 ? HQ_R(T, 1) : HQ_R(T, 32)
   switch (out_dt) {
     case DT_F32: HQ_D(F32);
     case DT_F16: HQ_D(F16);
     case DT_BF16: HQ_D(BF16);
   }
 #undef HQ_D
+#undef HQ_R
   return hipErrorInvalidValue;
 }
 

@@ -78,6 +78,33 @@ __device__ inline void rotate_lanes(float (&v)[8], int lane) {
   for (int m = 1; 8 * m < K; m <<= 1) fwht_xlane(v, lane, m);
 }
 
+// A butterfly stage over lanes l and l ^ M (M = 16 or 32) of two values at once: swapping a's upper lanes with
+// b's lower ones puts the halves of a into the lower lanes and those of b into the upper ones, so one sum and one
+// difference serve both; a second swap puts them back. The same sums as fwht_xlane_c, without the LDS permute.
+template <int M>
+__device__ inline void swap_lanes(uint32_t& a, uint32_t& b) {
+  const auto r = M == 16 ? __builtin_amdgcn_permlane16_swap(a, b, false, false) : __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+template <int M>
+__device__ inline void fwht_swap(float& a, float& b) {
+  uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
+  swap_lanes<M>(x, y);
+  const float s = __uint_as_float(x) + __uint_as_float(y), d = __uint_as_float(x) - __uint_as_float(y);
+  x = __float_as_uint(s), y = __float_as_uint(d);
+  swap_lanes<M>(x, y);
+  a = __uint_as_float(x);
+  b = __uint_as_float(y);
+}
+// The larger of lanes l and l ^ M, in both.
+template <int M>
+__device__ inline uint32_t swap_max(uint32_t x) {
+  uint32_t y = x;
+  swap_lanes<M>(x, y);
+  return max(x, y);
+}
+
 // Largest of the four lanes of a quad, in all of them.
 __device__ inline uint32_t quad_max(uint32_t x) {
   x = max(x, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), 0xB1, 0xF, 0xF, false)));
