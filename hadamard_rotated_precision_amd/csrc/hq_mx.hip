@@ -7,7 +7,9 @@
 // nearest to v / s without an intermediate rounding.
 //
 // What bounds it: bytes. R x C elements of e bytes are read once, 17/32 R C bytes are written for
-// each layout.
+// each layout: both from 8192 x 13824 bf16, rotated, take 100 us to nearest (347 MB, 3.5 TB/s) and 186
+// rounded at random, where the vector pipe is the bound (the two hashes' multiplications at a quarter
+// of its rate, for each pair and layout); the way back 45 us (286 MB, 6.4 TB/s, in part out of caches).
 #include "hq_device.hpp"
 #include "hq_launch.hpp"
 #include "hq_mx_device.hpp"
@@ -188,7 +190,8 @@ static hipError_t launch_quant(const MxQuantPass& p, const MxQuantArgs& a, hipSt
   const dim3 block(256);
   if (p.codes_t)
     return launch_k(mx_quant_kernel<T, ROT, RANDOM>, dim3(static_cast<unsigned>(tiles_r * a.tiles_c)), block, st, tok, a);
-  // four rows a thread once one row a thread would fill the chip twice over
+  // four rows a thread once one row a thread would fill the chip twice over: on the way back from
+  // 8192 x 13824 one took 80 us, four 45
   const int64_t span = (p.cols + 2047) / 2048;
   if (p.rows * span >= 4096)
     return launch_k(mx_quant_rows_kernel<T, ROT, RANDOM, 4>, dim3(static_cast<unsigned>((p.rows + 3) / 4 * span)), block, st, tok, a);

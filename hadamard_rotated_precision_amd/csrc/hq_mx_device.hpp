@@ -30,12 +30,13 @@ __device__ inline uint32_t mx_row_key(uint32_t seed, int64_t row) {
   return mix32(seed + 2654435761u * static_cast<uint32_t>(row));
 }
 
-// Magnitude code of x = |v| / s, rounded at random with the 16 bits u: from 1 on the significand's
-// dropped 22 bits plus 64 u carry into the kept one, below 1 the step is uniform.
-__device__ inline uint32_t mx_random_code(float x, uint32_t u) {
-  const uint32_t high = ((__float_as_uint(x) + (u << 6)) >> 22) - 252u;
-  const float low = __builtin_fmaf(x, 2.0f, static_cast<float>(u) * (1.0f / 65536.0f));
-  return x >= 1.0f ? high : static_cast<uint32_t>(static_cast<int>(low));
+// y = 2 v / s, rounded at random with the 16 bits u to twice a value that E2M1 has, toward zero after u
+// is added to the magnitude: from |y| = 2 on to the significand's dropped 22 bits, 64 u of their
+// 2^22 carrying into the kept one, below it to the fraction, for the step is uniform there.
+__device__ inline float mx_random(float y, uint32_t u) {
+  const float high = __uint_as_float((__float_as_uint(y) + (u << 6)) & 0xFFC00000u);
+  const float low = __builtin_truncf(__builtin_fmaf(static_cast<float>(u), copysignf(1.0f / 65536.0f, y), y));
+  return fabsf(y) >= 2.0f ? high : low;
 }
 
 // Eight codes, packed low first. key, pair: the row's key and half the first column's index.
@@ -43,13 +44,18 @@ template <bool RANDOM>
 __device__ inline uint32_t mx_codes8(const float (&v)[8], int byte, uint32_t key, uint32_t pair) {
   uint32_t w = 0;
   if constexpr (RANDOM) {
-    const float r = __uint_as_float(static_cast<uint32_t>(254 - byte) << 23);   // 1 / s, exact
+    const float r = __uint_as_float(static_cast<uint32_t>(255 - byte) << 23);   // 2 / s, exact
+    float y[8];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint32_t h = mix32(key ^ (pair + j));
-      w |= (mx_random_code(fabsf(v[2 * j]) * r, h & 0xFFFFu) | ((__float_as_uint(v[2 * j]) >> 28) & 8u)) << (8 * j);
-      w |= (mx_random_code(fabsf(v[2 * j + 1]) * r, h >> 16) | ((__float_as_uint(v[2 * j + 1]) >> 28) & 8u)) << (8 * j + 4);
+      y[2 * j] = mx_random(v[2 * j] * r, h & 0xFFFFu);
+      y[2 * j + 1] = mx_random(v[2 * j + 1] * r, h >> 16);
     }
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, y[0], y[1], 2.0f, 0);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, y[2], y[3], 2.0f, 1);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, y[4], y[5], 2.0f, 2);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, y[6], y[7], 2.0f, 3);
   } else {
     const float s = mx_scale(byte);
     w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[0], v[1], s, 0);
