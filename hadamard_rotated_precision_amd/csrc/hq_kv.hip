@@ -4,7 +4,8 @@
 // each block quantized as hq_mx.hip does: D / 8 lanes hold eight elements each, so strides 1, 2, 4
 // are in registers, the others across lanes, and a block's largest magnitude is that of a quad.
 //
-// What bounds it: bytes; for a decode batch, the launch.
+// What bounds it: bytes (16384 tokens of 8 heads of 128, bf16: 85 MB in 25 us each way, 3.4 TB/s); for
+// a decode batch, the launch (48 tokens: 3 us).
 #include "hq_device.hpp"
 #include "hq_kv_index.hpp"
 #include "hq_launch.hpp"

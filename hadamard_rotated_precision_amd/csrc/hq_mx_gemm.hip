@@ -5,7 +5,8 @@
 // lane: row lane % 16, the block of group lane / 16. It scales and adds by itself, so nothing but the
 // loads stands beside it. Products and the sums of a block are exact (multiples of 1/4 below 2^11);
 // its sum of 128 products was within 2^-25 of the sum of their magnitudes on random codes and scales.
-// P is the operand along the accumulator's registers (b: output columns, four consecutive ones per
+// What bounds it: at 16384^3 the matrix instruction (4.4 PFLOP/s), at 8192^3 (3.75) that and a whole
+// number of rounds of tiles. P is the operand along the accumulator's registers (b: output columns, four consecutive ones per
 // lane), Q the one along the lanes (a: output rows).
 #include "hq_device.hpp"
 #include "hq_launch.hpp"
@@ -132,8 +133,9 @@ __global__ __launch_bounds__(64 * NWP * NWQ * KS, 2) void mx_gemm_kernel(MxGemmA
     for (int l = 0; l < NDMA; ++l) load_piece(kt, stg, l, bp, bq);
   };
   // a lane's blocks are 2 lg and 2 lg + 1 of the step's eight, the same for both operands. The swizzle is
-  // that of row lr for every tile of 16 rows, so a lane has two offsets and a tile adds a constant (with an
-  // address for each tile the registers run out: scratch loads in the loop, 8192^3 365 against 340 us)
+  // that of row lr for every tile of 16 rows, so a lane has two offsets and a tile adds a constant (with
+  // an address for each tile the registers ran out and the loop read scratch memory: 8192^3 took 364 us,
+  // now 293, 3.75 PFLOP/s)
   const int at0 = lds_at(lr, 2 * lg), at1 = lds_at(lr, 2 * lg + 1), at_s = lr * 8 + 2 * lg;
   auto frag = [&](const int8_t* base, const int8_t* scales, int tile) {
     Fragment f;
@@ -314,11 +316,14 @@ static hipError_t launch_tiled(const MxGemmArgs& a, hipStream_t st, int tok, int
 }
 
 // Tile size by the time it would take, in microseconds per 256 of K on whole rounds and on ones with
-// fewer workgroups per compute unit (256 x 256: one fits; 128 x 128: two; 64 x 64: four).
+// fewer workgroups per compute unit (256 x 256: one fits; 128 x 128: two; 64 x 64: four): the rest's
+// from one round as K grows from 8192 to 16384, the whole rounds' from products of several. Tiles of
+// 64, 128 and 256 take 13.7, 16.5 and 30 us at 512 x 4096 x 4096, 24, 18 and 31 at 1000 x 4096 x 4096,
+// 97, 60 and 42 at 1000 x 13824 x 5120; those of 128 and 256 445 and 294 us at 8192 x 5120 x 13824.
 static int pick_tile(int64_t M, int64_t N) {
   constexpr int kCus = 256;
   struct Shape { int size, fit; double us[4]; };
-  static const Shape shapes[] = {{256, 1, {1.65}}, {128, 2, {0.75, 1.13}}, {64, 4, {0.32, 0.55, 0.72, 0.9}}};
+  static const Shape shapes[] = {{256, 1, {2.1}}, {128, 2, {0.8, 1.6}}, {64, 4, {0.45, 0.6, 0.85, 1.4}}};
   int best = 0;
   double best_us = 0.0;
   for (const Shape& s : shapes) {
@@ -331,16 +336,18 @@ static int pick_tile(int64_t M, int64_t N) {
 }
 
 // Splits of K over workgroups where 64 x 64 tiles leave most of the chip idle and K is long. With
-// the tiles' two groups of waves a step takes 512 of K: 0.55 us with one workgroup to a compute
-// unit, 1.0 with two; joining costs a launch and the splits' sums, written and read in fp32.
+// the tiles' two groups of waves a step takes 512 of K: 0.85 us with one workgroup to a compute
+// unit, 1.2 with two; joining costs a launch (4 us beside a short product) and the splits' sums,
+// written and read in fp32. 1, 2, 4, 8 and 16 splits of 64 x 1024 x 16384 take 26, 17, 12.5, 11.6 and
+// 13.2 us, of 64 x 4096 x 4096 9.3, 10.4, 10.9, 13.5 and 21.
 static int pick_splits(int64_t M, int64_t N, int64_t K) {
   const int64_t tiles = ((M + 63) / 64) * ((N + 63) / 64), steps = (K + 511) / 512;
   if (tiles > 256 || steps < 2) return 1;
   int best = 1;
   double best_us = 0.0;
   for (int s = 1; s <= 16 && tiles * s <= 512; ++s) {
-    const double us = static_cast<double>((steps + s - 1) / s) * (tiles * s <= 256 ? 0.55 : 1.0) +
-                      (s > 1 ? 3.0 + static_cast<double>(s) * M * N * 8.0 / 4e6 : 0.0);
+    const double us = static_cast<double>((steps + s - 1) / s) * (tiles * s <= 256 ? 0.85 : 1.2) +
+                      (s > 1 ? 4.0 + static_cast<double>(s) * M * N * 8.0 / 1.5e6 : 0.0);
     if (s == 1 || us < best_us) best = s, best_us = us;
   }
   // no split without work

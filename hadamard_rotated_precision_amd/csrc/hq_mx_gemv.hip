@@ -1,7 +1,8 @@
 // hq_mx_gemv.hip — microscaled 4-bit product for a few output rows (at most 32 tokens):
 //   c[m][n] (+)= alpha sum_kb 2^(ea(m,kb) + eb(n,kb)) sum_{k in kb} a[m][k] b[n][k]
 //
-// What bounds it: the bytes of b, read once, and the launch, first loads and joining. A workgroup
+// What bounds it: the bytes of b, read once, and the launch, first loads and joining (one token at
+// 11008 x 4096, fused: 24 MB in 8.7 us, 2.8 TB/s, launch included). A workgroup
 // takes 16 RT rows of b and the whole contraction; its eight waves take every eighth step of 256 K
 // each. A wave's fragments come straight from memory into the operand registers, kMvAhead steps ahead
 // of their use; the tokens are the lanes' side of v_mfma_scale_f32_16x16x128_f8f6f4, padded to 16 or
@@ -189,10 +190,14 @@ __global__ __launch_bounds__(64 * kMvWaves) void mx_gemv_kernel(MxGemvArgs g) {
   }
 }
 
-// Up to 16 tokens; 17 to 32 while every compute unit gets one workgroup at most (N <= 16 x 256) and
-// the tokens are few and short enough, for each workgroup reads all of their codes.
+// Where this kernel is faster than the tiles of hq_mx_gemm.hip: up to 16 tokens while every compute
+// unit gets one workgroup of 32 rows at most (N <= 32 x 256; 16 x 5120 x 5120 7.4 against 10.3 us,
+// 16 x 11008 x 4096 13.8 against 10.8, 1 x 32000 x 4096 20.6 against 17.4), 17 to 32 while that holds
+// with 16 rows and the tokens are few and short enough, for each workgroup reads all of their codes
+// (32 x 4096 x 4096 7.9 against 9.2 us, 24 x 4096 x 11008 13.1 against 12.7).
 bool mx_gemv_ok(int64_t M, int64_t N, int64_t K) {
-  return M >= 1 && K >= 1 && (M <= 16 || (M <= 32 && N <= 16 * 256 && M * K <= int64_t{3} << 16));
+  return M >= 1 && K >= 1 &&
+         ((M <= 16 && N <= 32 * 256) || (M <= 32 && N <= 16 * 256 && M * K <= int64_t{3} << 16));
 }
 
 // Fused when the tokens' codes fit their LDS.
@@ -212,14 +217,14 @@ static hipError_t launch_gemv(const MxGemvArgs& a, bool fused, hipStream_t st, i
 
 template <class Out>
 static hipError_t launch_rows(const MxGemvArgs& a, bool fused, hipStream_t st, int tok) {
-  // 16 rows of b per workgroup while all workgroups are on the chip at once (three to a compute
-  // unit), else 32
+  // 16 rows of b per workgroup while every compute unit gets one at most, else 32: one token at
+  // 4096 x 11008 9.0 and 11.3 us, 16 at 5120 x 5120 9.2 and 7.4
   if (a.M > 16) return launch_gemv<Out, 1, 2>(a, fused, st, tok);
-  return a.N > 16 * 3 * 256 ? launch_gemv<Out, 2, 1>(a, fused, st, tok) : launch_gemv<Out, 1, 1>(a, fused, st, tok);
+  return a.N > 16 * 256 ? launch_gemv<Out, 2, 1>(a, fused, st, tok) : launch_gemv<Out, 1, 1>(a, fused, st, tok);
 }
 
 hipError_t mx_gemv_pass(const MxGemmPass& p, const void* x, int x_dt, int rot, hipStream_t st) {
-  if (!mx_gemv_ok(p.M, p.N, p.K) || (x && !mx_gemv_fused_ok(p.M, p.K))) return hipErrorInvalidValue;
+  if (x ? !mx_gemv_fused_ok(p.M, p.K) : !mx_gemv_ok(p.M, p.N, p.K)) return hipErrorInvalidValue;
   const MxGemvArgs a{p.b, p.a, x, static_cast<int>(p.M), p.N, static_cast<int>(p.K), x_dt, rot, p.alpha, p.c, p.accumulate};
   const int tok = prof_open(K_GEMM, 2.0 * p.M * p.N * p.K);
   switch (p.out_dt) {
