@@ -26,6 +26,8 @@
 // Precision: fp32 statistics, scores and accumulators. Of the largest in its block of 32, a query is
 // kept to 2^-18 (QN = 4) or 2^-28 (6; fp32 in or out). Probabilities are split into PN bf16 numbers:
 // to 2^-17 (2) or 2^-25 (3).
+#include <algorithm>
+
 #include "hq_device.hpp"
 #include "hq_kv_index.hpp"
 #include "hq_launch.hpp"
@@ -856,16 +858,7 @@ __device__ __forceinline__ void attend(const KvAttnArgs& g, const KvTile& tile, 
 #pragma unroll
           for (int j = 0; j < 8; ++j) v[j] += from_wave[j];
         }
-        if (part_at < 0) {
-          finish_row<D>(g, tile, tile.r0 + r, i, total, low, tile.r0 + r < tile.rows, v);
-        } else {
-          const int64_t at = part_at * g.tile_rows + r;
-          store8<F32>(g.part, at * D + 8 * i, 8, v);
-          if (i == 0) {
-            g.stats[2 * at] = big;
-            g.stats[2 * at + 1] = total;
-          }
-        }
+        finish_row<D>(g, tile, tile.r0 + r, i, total, low, tile.r0 + r < tile.rows, v);
       }
     }
   }
@@ -1000,9 +993,18 @@ __global__ __launch_bounds__(64 * kWaves) void kv_join_kernel(KvAttnArgs g, int 
   else if (w0 != w1) join_parts<D>(g, tile, row0, 2 * w0 + 1, 2 * (w0 + 1), 2, static_cast<int>(w1 - w0 + 1));
 }
 
-// How a call is cut up. Rows of a sequence and head: up to 64 (32 with 256 elements) a workgroup or wave takes
-// 32 (16) of them with all their tokens or a part of them; more: each wave of a workgroup has 32 (16) of
-// its own, and the tokens may be split.
+// How a call is cut up. Rows of a sequence and head: up to 64 (32 with 256 elements) a workgroup or wave
+// takes 32 (16) of them with all their tokens or a part of them; more: each wave of a workgroup has 32 (16)
+// of its own, and the tokens may be split. Measured, in us, sequences of lengths up to L, 8 heads of the
+// cache, groups of 4, D = 128, bf16:
+//   single tokens, waves sharing the rows against the line (which costs a joining kernel and a walk over
+//     the sequences, but fills the chip): 1 sequence, L = 2048 18.9, 21.5, 4096 30, 22; 8 sequences, 3000
+//     25, 29, 8192 57, 38; 32, 4096 36, 44, 16384 120, 90; 128, 8192 160, 193, 16384 300, 306
+//   the least piece of the line 2, 4, 8, 16 chunks: 1 sequence, 4096 21, 23, 29, -, 32768 45, 34, 35, 45
+//   8 tokens (32 rows), shared, line, own rows: 1 sequence, 1000 19, 25, 23, 2000 28, 26, 23; 8 sequences,
+//     1000 19, 35, 28, 4096 -, 51, 39; 32, 4096 51, 72, 101, 16384 175, 142, 324
+//   own rows, split to 256, 512, 1024 workgroups: 500 tokens behind 7500, 171, 140, 154; 4 x 64 tokens of
+//     16000, 167, 106, 129
 struct KvPlan {
   int mode;
   int rt;
@@ -1017,24 +1019,29 @@ static KvPlan kv_plan(const hq_kv_cache& c, const hq_kv_batch& b) {
   KvPlan p = {};
   const int64_t rows = static_cast<int64_t>(b.max_q) * (b.q_heads / c.heads);
   const bool few = rows <= (c.head_dim == 256 ? 32 : 64);
-  p.mode = few ? MERGED : OWN_ROWS;
+  const int64_t seen = b.window ? std::min<int64_t>(b.max_len, static_cast<int64_t>(b.window) + b.max_q) : b.max_len;
+  const int64_t chunks = (seen + kChunk - 1) / kChunk + 1;
+  const int64_t fit = 256 * (c.head_dim == 64 ? 3 : c.head_dim == 128 ? 2 : 1);   // workgroups on the chip
   p.rt = c.head_dim < 256 && rows > 16 ? 2 : 1;
-  p.tile_rows = 16 * p.rt * (few ? 1 : kWaves);
-  p.tiles = (rows + p.tile_rows - 1) / p.tile_rows;
-  p.work = static_cast<int64_t>(b.seqs) * c.heads * p.tiles;
-  p.splits = 1;
-  p.grid = p.work;
-  const int64_t chunks = (static_cast<int64_t>(b.max_len) + kChunk - 1) / kChunk + 1;
-  if (few) {
-    const int64_t fit = 256 * (c.head_dim == 64 ? 3 : c.head_dim == 128 ? 2 : 1);   // workgroups on the chip
-    if (chunks > 4 * kWaves && p.work < 8 * fit) {
-      p.mode = ALONE;
-      p.least = 2;
-      const int64_t most = (p.work * chunks + p.least * kWaves - 1) / (p.least * kWaves);
-      p.grid = most < fit ? most : fit;
-      p.parts = 2 * kWaves * p.grid;
-    }
-  } else {
+  auto shape = [&](int mode) {
+    p.mode = mode;
+    p.tile_rows = 16 * p.rt * (mode == OWN_ROWS ? kWaves : 1);
+    p.tiles = (rows + p.tile_rows - 1) / p.tile_rows;
+    p.work = static_cast<int64_t>(b.seqs) * c.heads * p.tiles;
+    p.grid = p.work;
+    p.splits = 1;
+  };
+  shape(few ? MERGED : OWN_ROWS);
+  // (a wave counts its chunks in 32 bits)
+  if (few && chunks > 48 + 128 * p.work / fit && p.work * chunks < int64_t{1} << 40) shape(ALONE);
+  if (few && rows > 16 && chunks > 32 && p.work <= 64) shape(OWN_ROWS);
+  if (p.mode == ALONE) {
+    p.least = 4;
+    const int64_t most = (p.work * chunks + p.least * kWaves - 1) / (p.least * kWaves);
+    p.grid = most < fit ? most : fit;
+    p.parts = 2 * kWaves * p.grid;
+  }
+  if (p.mode == OWN_ROWS) {
     const int64_t most = (chunks + 3) / 4;
     int64_t s = p.work > 0 ? 512 / p.work : 1;      // two workgroups to a compute unit
     s = s < most ? s : most;

@@ -848,7 +848,7 @@ class KVCache:
         return b
 
     def attention_workspace(self, seqs, q_heads, max_q, max_len):
-        """A workspace for attend() with these bounds."""
+        """A workspace for attend() with these bounds and any window."""
         size = B.hq_kv_attention_workspace_bytes(self.st, self._batch(seqs, q_heads, max_q, max_len))
         return torch.empty(max(size, 16), dtype=torch.uint8, device=self.device)
 

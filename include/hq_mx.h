@@ -27,8 +27,8 @@
  *     overlap neither inputs nor each other.
  *   - All argument checks run before any launch; on error nothing is launched or written.
  *   - Results do not depend on the order in which workgroups run: the same call on the same data
- *     gives the same bits. They do depend on the shapes: another number of rows, or another bound
- *     on the lengths, may take another order of summation.
+ *     gives the same bits. They do depend on the shapes: another number of rows, another bound on
+ *     the lengths, or other lengths of the sequences beside it, may take another order of summation.
  *   - hq_profile_start's kinds: products and attention HQ_KIND_GEMM, quantizing and appending
  *     HQ_KIND_ROT_QUANT, reading back HQ_KIND_ROT_STORE, the joining of split sums HQ_KIND_MISC.
  */
@@ -195,7 +195,8 @@ typedef struct {
   float scale;     /* of the dot products, before the softmax */
 } hq_kv_batch;
 
-/* Bytes of hq_kv_attention's workspace for these bounds (0 where there is nothing to split). */
+/* Bytes of hq_kv_attention's workspace for these bounds (0 where there is nothing to split). A window
+ * needs no more than none. */
 size_t hq_kv_attention_workspace_bytes(const hq_kv_cache *cache, const hq_kv_batch *batch);
 
 /* out = softmax(scale q K^T) V. Query row i of a sequence with n rows and length len stands at
@@ -204,9 +205,12 @@ size_t hq_kv_attention_workspace_bytes(const hq_kv_cache *cache, const hq_kv_bat
  * q[t * q_token + h * q_head + d]; out: tokens x q_heads x head_dim, contiguous, dtype out_dtype. Rows
  * of `tokens` that belong to no sequence are left as they are. lse: NULL, or tokens x q_heads fp32
  * logarithms of the sums of exp(scale q k).
- * Sums, maxima and accumulators are fp32. Queries and probabilities enter the 16-bit matrix
- * instruction in parts: two bf16 numbers each (their sum is within 2^-17 of the value), three
- * (2^-25) where q or out is fp32; codes are exact there. */
+ * Sums, maxima and accumulators are fp32. Queries enter the matrix instruction beside the keys' codes,
+ * in parts of 6 bits with a scale for each block of 32: four parts (their sum is within 2^-18 of the
+ * block's largest magnitude), six (2^-28) where q or out is fp32. Probabilities enter it as two bf16
+ * numbers (their sum is within 2^-17 of the value) or three (2^-25) beside the values, which are exact
+ * in bf16.
+ * Sequences' query rows must not overlap (their results would). */
 hq_status hq_kv_attention(const void *q, int32_t q_dtype, int64_t tokens, int64_t q_token,
                           int64_t q_head, const hq_kv_cache *cache, const hq_kv_batch *batch,
                           void *out, int32_t out_dtype, float *lse, void *ws, size_t ws_bytes,

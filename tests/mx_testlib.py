@@ -156,10 +156,17 @@ def fill(cache, g, spread=4.0):
 def attention(cache, q, starts, lens, table, scale, window, dtype):
     """(out, lse, bound of out, bound of lse) in 64 bits, rows of no sequence as NaN.
 
-    The bounds count, for parts = bf16 numbers that a query or probability is split into (3 with fp32
-    in or out: 2^-25, else 2^-17) and a row that sees n tokens:
+    The bounds count, for parts = bf16 numbers that a probability is split into (3 with fp32 in or out:
+    2^-25, else 2^-17) and a row that sees n tokens:
       scores    q: its rotation (log2 D stages and the scaling, each half a step of sums below sum |q|
                 in magnitude), its split; the products' sum: parts D additions. d_j below.
+                The split into 6-bit numbers (E2M3: steps of 1/8 below 2, 1/4 below 4, 1/2 up to 7.5),
+                each with a scale s of the block of 32, the smallest power of two with max |q| <= 7.5 s,
+                so s < max |q| / 3.75. The first leaves at most s / 4, which is 4 of the second's
+                s / 16; that leaves 1/8 of its scale, 4 of the third's at 2^-5 of it, and so on. After
+                four: s 2^(-3 - 4 - 5 - 5) = s 2^-17, below 2^-18 max |q|; after six (fp32): s 2^-27,
+                below 2^-28 max |q|. It is relative to the block's largest, so an element's error is
+                multiplied with |k| by itself.
       p_j       the score's error d_j, the rounding of s_j - m (in powers of two, twice half a step of
                 |s_j| + |m|), the exponential's two steps, its split: e_j.
       sums      n + 64 additions in fp32 for each part, of sums below sum p |v|, and the same for l.
@@ -199,7 +206,9 @@ def attention(cache, q, starts, lens, table, scale, window, dtype):
             sj = torch.mm(x, kz.t().contiguous()) * (scale / rot)
             big = torch.mm(x.abs(), kz.abs().t().contiguous()) * sc
             total = q[a:b, h].double().abs().sum(-1, keepdim=True) if rot > 1 else x.abs().amax(-1, keepdim=True)
-            d = big * (cut + parts * D * u) + total * kz.abs().sum(-1) * sc * stages * u
+            largest = x.abs().unflatten(-1, (-1, 32)).amax(-1).repeat_interleave(32, -1)
+            split = torch.mm(largest, kz.abs().t().contiguous()) * sc * 2.0 ** (-28 if parts == 3 else -18)
+            d = split + big * parts * D * u + total * kz.abs().sum(-1) * sc * stages * u
             sj = sj.masked_fill(~seen, -math.inf)
             m = sj.amax(-1, keepdim=True)
             some = seen.any(-1)

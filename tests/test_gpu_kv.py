@@ -174,6 +174,39 @@ def test_attention(news, lens, D, heads, group, page, dtype, rotate):
     check(cache, q, starts, lens, table)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("seqs,heads,group,new,longest",
+                         [(3, 2, 4, 1, 9000), (300, 1, 3, 1, 13000), (40, 2, 4, 5, 6200), (40, 2, 12, 5, 13000),
+                          (2, 2, 8, 5, 2500)])
+def test_long_lengths_among_short_ones(seqs, heads, group, new, longest, D, dtype):
+    """One long sequence, the others short, of length 0 or without new tokens: the pieces of the waves
+    begin and end anywhere, and hold many sequences or a part of one."""
+    g = gen(seqs + D)
+    lens = [(37 * s) % 150 for s in range(seqs)]
+    lens[seqs // 2], lens[-1] = longest, 0
+    news = [min(new, n) if s % 7 else 0 for s, n in enumerate(lens)]
+    news[seqs // 2] = new
+    page = 64
+    cache = R.new_cache(sum(-(-n // page) for n in lens) + 3, page, heads, D)
+    R.fill(cache, g, 2.0)
+    starts, table = R.batch(g, cache, news, lens)
+    q = heads_of(g, starts[-1], heads * group, D, dtype, False)
+    check(cache, q, starts, lens, table)
+    check(cache, q, starts, lens, table, window=longest - 1000)
+    if seqs < 100:      # two long ones, and every bound at once
+        lens[0], news[0] = longest - 77, 0
+        lens[1] = longest // 2
+        cache = R.new_cache(sum(-(-n // page) for n in lens) + 3, page, heads, D, False)
+        R.fill(cache, g, 2.0)
+        starts, table = R.batch(g, cache, news, lens)
+        q = heads_of(g, starts[-1], heads * group, D, dtype, False)
+        out, _ = check(cache, q, starts, lens, table)
+        for wrong in ([5] + starts[1:], [-4] + starts[1:], starts[:-1] + [2 ** 31 - 1], starts[::-1]):
+            run(cache, q, wrong, [n * 3 - 70 for n in lens], table, max_q=new, max_len=longest)
+        torch.cuda.synchronize()
+
+
 @pytest.mark.parametrize("window", [1, 2, 33, 64, 200, 5000])
 @pytest.mark.parametrize("D", [64, 128])
 def test_windows(window, D):

@@ -3,6 +3,7 @@ addresses; every call below fails its argument checks, or stops at the device ch
 launch."""
 import ctypes
 import os
+import random
 import re
 import subprocess
 import sys
@@ -287,3 +288,15 @@ def test_no_call_reaches_the_device_where_there_is_one(tmp_path):
     assert r.returncode == 0
     tail = r.stdout.strip().splitlines()[-1]
     assert "passed" in tail and "skipped" in tail
+
+
+@pytest.mark.skipif("HQ_MX_LIB_PATH" in os.environ, reason="the sanitizer build has no launchers of its own")
+def test_a_window_needs_no_more_workspace_than_none():
+    rng = random.Random(1)
+    for _ in range(3000):
+        c = cache(head_dim=rng.choice([64, 128, 256]), heads=rng.choice([1, 2, 8, 16]), rot=1)
+        b = dict(seqs=rng.choice([1, 2, 5, 33, 300]), q_heads=c.heads * rng.choice([1, 4, 12]),
+                 max_q=rng.choice([1, 3, 9, 70, 1000]), max_len=int(2 ** rng.uniform(0, 18)))
+        without = B.hq_kv_attention_workspace_bytes(c, batch(**b))
+        window = int(2 ** rng.uniform(0, 18))
+        assert B.hq_kv_attention_workspace_bytes(c, batch(window=window, **b)) <= without, (b, window)
