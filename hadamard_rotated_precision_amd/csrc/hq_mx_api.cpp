@@ -162,7 +162,7 @@ bool stride_ok(int64_t s) { return s >= 0 && s <= (int64_t{1} << 40); }
 hq_status check_batch(const hq_kv_cache& c, const hq_kv_batch* b) {
   if (!b) return HQ_ERR_NULL;
   if (b->seqs < 0 || b->max_q < 0 || b->max_len < 0 || b->table_ld < 0 || b->window < 0) return HQ_ERR_SHAPE;
-  if (b->table_ld > (int64_t{1} << 31)) return HQ_ERR_SHAPE;
+  if (b->table_ld > (int64_t{1} << 31) || b->max_len > (1 << 30)) return HQ_ERR_SHAPE;
   if (b->q_heads < 1 || b->q_heads % c.heads || b->q_heads / c.heads > 1024) return HQ_ERR_MISMATCH;
   // workgroups and partial results of a call stay countable
   if (static_cast<int64_t>(b->max_q) * (b->q_heads / c.heads) > (int64_t{1} << 27) ||

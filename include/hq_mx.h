@@ -182,10 +182,10 @@ hq_status hq_kv_read(const hq_kv_cache *cache, const int64_t *slots, int64_t n, 
  *   q_starts  seqs + 1: the query rows of sequence s are q_starts[s] .. q_starts[s + 1]
  *   lens      seqs: tokens of the sequence in the cache, its new ones (already appended) among them
  *   table     seqs x table_ld: the page of its tokens [p * page, (p + 1) * page)
- * max_q, max_len: bounds on the numbers of query rows and on the lengths, known on the host; rows
- * and tokens beyond them are not computed and not seen. A page outside [0, pages), or past table_ld,
- * is not seen either; query rows outside the tensor are not touched. (A server's own mistake in
- * these arrays gives wrong answers, but no access outside the buffers.) */
+ * max_q, max_len: bounds on the numbers of query rows and on the lengths (at most 2^30), known on the
+ * host; rows and tokens beyond them are not computed and not seen. A page outside [0, pages), or past
+ * table_ld, is not seen either; query rows outside the tensor are not touched. (A server's own mistake
+ * in these arrays gives wrong answers, but no access outside the buffers.) */
 typedef struct {
   const int32_t *q_starts, *lens, *table;
   int64_t table_ld;

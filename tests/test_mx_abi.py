@@ -248,6 +248,7 @@ def batch(**kw):
     ({}, dict(seqs=-1), {}, "HQ_ERR_SHAPE"),
     ({}, dict(max_q=-1), {}, "HQ_ERR_SHAPE"),
     ({}, dict(max_len=-1), {}, "HQ_ERR_SHAPE"),
+    ({}, dict(max_len=(1 << 30) + 1), {}, "HQ_ERR_SHAPE"),
     ({}, dict(table_ld=-1), {}, "HQ_ERR_SHAPE"),
     ({}, dict(window=-1), {}, "HQ_ERR_SHAPE"),
     ({}, dict(q_heads=12), {}, "HQ_ERR_MISMATCH"),
