@@ -2,7 +2,7 @@
 //   o_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(scale q_i . k_j - m_i),
 // in one pass over the cache with running maxima m and sums.
 //
-// A wave takes 16 RT query rows of one sequence and one head of the cache (a group of query heads
+// A wave takes 16 RT (RT = 1 or 2) query rows of one sequence and one head of the cache (a group of query heads
 // times a few tokens) through chunks of 64 tokens. The products are transposed, S^T = K Q^T and
 // O^T = V^T P^T, so that a lane keeps one query row throughout (lane % 16): the statistics of a row
 // are a lane's own, and the probabilities leave the first product in the very registers that the
@@ -428,9 +428,11 @@ __device__ __forceinline__ uint32_t widen2(uint32_t w, uint32_t s) {
 // How the waves of a workgroup divide the work:
 //   OWN_ROWS  each has 16 RT rows of its own; all read the same chunk, of which each loads a tile
 //   MERGED    they share 16 RT rows and take every fourth chunk each; their sums meet in LDS
+//   MERGED8   the same with eight waves, where no compute unit has more than one workgroup
 //   ALONE     each has a piece of the line of chunks for itself
-// MERGED and ALONE have a part of each stage for every wave.
-enum KvMode { OWN_ROWS = 0, MERGED = 1, ALONE = 2 };
+// All but OWN_ROWS have a part of each stage for every wave.
+enum KvMode { OWN_ROWS = 0, MERGED = 1, ALONE = 2, MERGED8 = 3 };
+constexpr int waves_of(int mode) { return mode == MERGED8 ? 2 * kWaves : kWaves; }
 
 template <int D, int RT>
 struct KvShared {
@@ -445,6 +447,8 @@ struct KvShared {
 // go to that part of the workspace.
 template <int D, int RT, int QN, int PN, int MODE>
 __device__ __forceinline__ void attend(const KvAttnArgs& g, const KvTile& tile, int begin, int end, int64_t part_at, const KvShared<D, RT>& sh) {
+  constexpr int NW = waves_of(MODE);
+  constexpr bool MERGE = MODE == MERGED || MODE == MERGED8;
   constexpr int DT = D / 16;                        // 16-wide tiles of the output; elements a lane reads of a token of V
   using Stage = KvStage<D>;
   constexpr int KU = Stage::KU;
@@ -460,11 +464,11 @@ __device__ __forceinline__ void attend(const KvAttnArgs& g, const KvTile& tile, 
   const int r0 = tile.r0 + (MODE == OWN_ROWS ? w * ROWS : 0);     // of this wave
   const KvSequence& s = tile.s;
   const int wg_to = tile.end_token(g);
-  KvPages pages(g, tile, (begin + (MODE == MERGED ? w : 0)) * kChunk);
+  KvPages pages(g, tile, (begin + (MERGE ? w : 0)) * kChunk);
 
   // One chunk: its loads have landed (and, where the waves share it, everybody's), those of the next go
   // out into the other stage, whose last reads are done.
-  constexpr int STEP = MODE == MERGED ? kWaves : 1;
+  constexpr int STEP = MERGE ? NW : 1;
   const int part_of_stage = MODE == OWN_ROWS ? 0 : w * Stage::BYTES;
   int8_t *const s0 = st0 + part_of_stage, *const s1 = st1 + part_of_stage;
   int64_t row[4] = {-1, -1, -1, -1}, next[4] = {-1, -1, -1, -1};
@@ -488,7 +492,7 @@ __device__ __forceinline__ void attend(const KvAttnArgs& g, const KvTile& tile, 
     if (MODE != OWN_ROWS || w == 0) Stage::load_scales(g.k_scales, r, Stage::k_scales(to), lane);
     if (MODE != OWN_ROWS || w == 1) Stage::load_scales(g.v_scales, r, Stage::v_scales(to), lane);
   };
-  int c = begin + (MODE == MERGED ? w : 0);
+  int c = begin + (MERGE ? w : 0);
   if (c < end) {       // on their way while the queries are prepared
     pages.chunk(c * kChunk, wg_to, row);
     issue(row, s0);
@@ -511,8 +515,8 @@ __device__ __forceinline__ void attend(const KvAttnArgs& g, const KvTile& tile, 
       for (int j = 0; j < 8; ++j) to[j] = v[j] * g.sign;
     }
   };
-  if constexpr (MODE == MERGED) {
-    bring_rows(reinterpret_cast<float*>(st1), 0, ROWS, t, 64 * kWaves);
+  if constexpr (MERGE) {
+    bring_rows(reinterpret_cast<float*>(st1), 0, ROWS, t, 64 * NW);
     __syncthreads();
   }
 #pragma unroll
@@ -578,7 +582,7 @@ __device__ __forceinline__ void attend(const KvAttnArgs& g, const KvTile& tile, 
   }
 
   // the second stage is free again
-  if constexpr (MODE == MERGED) __syncthreads();
+  if constexpr (MERGE) __syncthreads();
 
   // tokens that this lane's rows see: [from, to); and those of all rows, and of any (of the wave: one whose
   // rows lie behind the last sees nothing)
@@ -789,7 +793,7 @@ __device__ __forceinline__ void attend(const KvAttnArgs& g, const KvTile& tile, 
     l[rt] += __shfl_xor(l[rt], 32, 64);
   }
 
-  if constexpr (MODE != MERGED) {
+  if constexpr (!MERGE) {
     // a lane holds D / 4 consecutive elements of a row, from D / 4 lg on
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
@@ -834,7 +838,7 @@ __device__ __forceinline__ void attend(const KvAttnArgs& g, const KvTile& tile, 
       __syncthreads();
       float top = sh.wave_m[0][16 * rt + lr];
 #pragma unroll
-      for (int i = 1; i < kWaves; ++i) top = fmaxf(top, sh.wave_m[i][16 * rt + lr]);
+      for (int i = 1; i < NW; ++i) top = fmaxf(top, sh.wave_m[i][16 * rt + lr]);
       const float f = __builtin_amdgcn_exp2f(sh.wave_m[w][16 * rt + lr] - (top == -__builtin_inff() ? 0.0f : top));
       float* const mine = reinterpret_cast<float*>(s0) + lr * QP;
 #pragma unroll
@@ -844,15 +848,15 @@ __device__ __forceinline__ void attend(const KvAttnArgs& g, const KvTile& tile, 
           *reinterpret_cast<v4f*>(mine + DT * (4 * lg + e) + d) =
               v4f{o[rt][d][e] * f, o[rt][d + 1][e] * f, o[rt][d + 2][e] * f, o[rt][d + 3][e] * f};
       __syncthreads();
-      for (int e = t; e < 16 * D / 8; e += 64 * kWaves) {
+      for (int e = t; e < 16 * D / 8; e += 64 * NW) {
         const int r = 16 * rt + e / (D / 8), i = e % (D / 8);
         float big = sh.wave_m[0][r];
 #pragma unroll
-        for (int k = 1; k < kWaves; ++k) big = fmaxf(big, sh.wave_m[k][r]);
+        for (int k = 1; k < NW; ++k) big = fmaxf(big, sh.wave_m[k][r]);
         const float low = big == -__builtin_inff() ? 0.0f : big;
         float total = 0.0f, v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int k = 0; k < kWaves; ++k) {
+        for (int k = 0; k < NW; ++k) {
           total += sh.wave_l[k][r] * __builtin_amdgcn_exp2f(sh.wave_m[k][r] - low);
           const float* const from_wave = reinterpret_cast<const float*>(st0 + k * Stage::BYTES) + (r - 16 * rt) * QP + 8 * i;
 #pragma unroll
@@ -865,11 +869,11 @@ __device__ __forceinline__ void attend(const KvAttnArgs& g, const KvTile& tile, 
 }
 
 template <int D, int RT, int QN, int PN, int MODE>
-__global__ __launch_bounds__(64 * kWaves, 2) void kv_attention_kernel(KvAttnArgs g) {
-  constexpr int PARTS = MODE == OWN_ROWS ? 1 : kWaves;
+__global__ __launch_bounds__(64 * waves_of(MODE), 2) void kv_attention_kernel(KvAttnArgs g) {
+  constexpr int NW = waves_of(MODE), PARTS = MODE == OWN_ROWS ? 1 : NW, HELD = MODE == MERGED || MODE == MERGED8 ? NW : 1;
   __shared__ __attribute__((aligned(16))) int8_t st0[PARTS * KvStage<D>::BYTES];
   __shared__ __attribute__((aligned(16))) int8_t st1[PARTS * KvStage<D>::BYTES];
-  __shared__ float wave_m[MODE == MERGED ? kWaves : 1][16 * RT], wave_l[MODE == MERGED ? kWaves : 1][16 * RT];
+  __shared__ float wave_m[HELD][16 * RT], wave_l[HELD][16 * RT];
   const KvShared<D, RT> sh{st0, st1, wave_m, wave_l};
   if constexpr (MODE != ALONE) {
     // one tile's tokens, or a split of them
@@ -881,8 +885,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attention_kernel(KvAttnArgs
     attend<D, RT, QN, PN, MODE>(g, tile, first + min(chunks, split * per), first + min(chunks, (split + 1) * per),
                                 g.splits > 1 ? static_cast<int64_t>(blockIdx.x) : -1, sh);
   } else {
-    const int wave = static_cast<int>(blockIdx.x) * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const KvLine line = kv_line(g, gridDim.x * kWaves, -1);
+    const int wave = static_cast<int>(blockIdx.x) * NW + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const KvLine line = kv_line(g, gridDim.x * NW, -1);
     // the same in all lanes: addresses and loops stay scalar
     int at = __builtin_amdgcn_readfirstlane(line.tile);
     if (at < 0) return;
@@ -994,20 +998,23 @@ __global__ __launch_bounds__(64 * kWaves) void kv_join_kernel(KvAttnArgs g, int 
 }
 
 // How a call is cut up. Rows of a sequence and head: up to 64 (32 with 256 elements) a workgroup or wave
-// takes 32 (16) of them with all their tokens or a part of them; more: each wave of a workgroup has 32 (16)
-// of its own, and the tokens may be split. Measured, in us, sequences of lengths up to L, 8 heads of the
+// takes 16 of them with all their tokens or a part of them; more: each wave of a workgroup has 32 (16) of
+// its own, and the tokens may be split. Measured, in us, sequences of lengths up to L, 8 heads of the
 // cache, groups of 4, D = 128, bf16:
-//   single tokens, waves sharing the rows against the line (which costs a joining kernel and a walk over
-//     the sequences, but fills the chip): 1 sequence, L = 2048 18.9, 21.5, 4096 30, 22; 8 sequences, 3000
-//     25, 29, 8192 57, 38; 32, 4096 36, 44, 16384 120, 90; 128, 8192 160, 193, 16384 300, 306
+//   single tokens; four waves that share the rows, eight (a workgroup to a compute unit), the line (which
+//     costs a joining kernel and a walk over the sequences, but fills the chip): 1 sequence, L = 1000 15.5,
+//     14.1, 23, 4096 30, 26, 25, 8192 53, 40, 24; 8 sequences, 4096 30, 24, 30, 8192 57, 45, 39; 32, 4096
+//     38, 31, 46, 8192 66, 50, 64, 16384 125, 96, 90; 64, 2000 30, 40, 50, 16384 165, -, 165; 128, 8192
+//     160, -, 193, 16384 300, -, 306
 //   the least piece of the line 2, 4, 8, 16 chunks: 1 sequence, 4096 21, 23, 29, -, 32768 45, 34, 35, 45
-//   8 tokens (32 rows), shared, line, own rows: 1 sequence, 1000 19, 25, 23, 2000 28, 26, 23; 8 sequences,
-//     1000 19, 35, 28, 4096 -, 51, 39; 32, 4096 51, 72, 101, 16384 175, 142, 324
+//   8 tokens (32 rows); the same three, and own rows: 1 sequence, 1000 14.4, 14.6, 24, 23, 4096 31, 26, 25,
+//     25; 8 sequences, 4096 35, 28, 40, 39; 32, 4096 50, 55, 65, 103, 16384 157, 171, 163, 325. Tiles of 32
+//     rows for the first three spill registers with fp32 and took, for 8 sequences of 4096, 45, 37, 46, for
+//     32 of 16384 169, 131, 142.
 //   own rows, split to 256, 512, 1024 workgroups: 500 tokens behind 7500, 171, 140, 154; 4 x 64 tokens of
 //     16000, 167, 106, 129
 struct KvPlan {
   int mode;
-  int rt;
   int tile_rows;
   int64_t tiles;      // of a sequence and head
   int64_t work;       // of the batch
@@ -1022,19 +1029,20 @@ static KvPlan kv_plan(const hq_kv_cache& c, const hq_kv_batch& b) {
   const int64_t seen = b.window ? std::min<int64_t>(b.max_len, static_cast<int64_t>(b.window) + b.max_q) : b.max_len;
   const int64_t chunks = (seen + kChunk - 1) / kChunk + 1;
   const int64_t fit = 256 * (c.head_dim == 64 ? 3 : c.head_dim == 128 ? 2 : 1);   // workgroups on the chip
-  p.rt = c.head_dim < 256 && rows > 16 ? 2 : 1;
   auto shape = [&](int mode) {
     p.mode = mode;
-    p.tile_rows = 16 * p.rt * (mode == OWN_ROWS ? kWaves : 1);
+    p.tile_rows = mode != OWN_ROWS ? 16 : 16 * kWaves * (c.head_dim < 256 ? 2 : 1);
     p.tiles = (rows + p.tile_rows - 1) / p.tile_rows;
     p.work = static_cast<int64_t>(b.seqs) * c.heads * p.tiles;
     p.grid = p.work;
     p.splits = 1;
   };
   shape(few ? MERGED : OWN_ROWS);
+  if (few && c.head_dim < 256 && p.work <= 256 && chunks > kWaves) shape(MERGED8);
   // (a wave counts its chunks in 32 bits)
-  if (few && chunks > 48 + 128 * p.work / fit && p.work * chunks < int64_t{1} << 40) shape(ALONE);
-  if (few && rows > 16 && chunks > 32 && p.work <= 64) shape(OWN_ROWS);
+  if (few && chunks > (p.mode == MERGED8 ? 52 + 7 * p.work / 10 : 48 + p.work / 4) &&
+      p.work * chunks < int64_t{1} << 40)
+    shape(ALONE);
   if (p.mode == ALONE) {
     p.least = 4;
     const int64_t most = (p.work * chunks + p.least * kWaves - 1) / (p.least * kWaves);
@@ -1062,21 +1070,24 @@ size_t kv_attention_ws(const hq_kv_cache& c, const hq_kv_batch& b) {
 
 template <int D, int RT, int MODE>
 static hipError_t launch_shape(const KvAttnArgs& a, const KvPlan& p, hipStream_t st, int tok) {
-  const dim3 grid(static_cast<unsigned>(p.grid)), block(64 * kWaves);
+  const dim3 grid(static_cast<unsigned>(p.grid)), block(64 * waves_of(MODE));
   if (a.q_dt == DT_F32 || a.out_dt == DT_F32) return launch_k(kv_attention_kernel<D, RT, 6, 3, MODE>, grid, block, st, tok, a);
   return launch_k(kv_attention_kernel<D, RT, 4, 2, MODE>, grid, block, st, tok, a);
 }
 
-template <int D, int RT>
-static hipError_t launch_few(const KvAttnArgs& a, const KvPlan& p, hipStream_t st, int tok) {
-  return p.mode == ALONE ? launch_shape<D, RT, ALONE>(a, p, st, tok) : launch_shape<D, RT, MERGED>(a, p, st, tok);
+template <int D>
+static hipError_t launch_mode(const KvAttnArgs& a, const KvPlan& p, hipStream_t st, int tok) {
+  if (p.mode == OWN_ROWS) return launch_shape<D, D < 256 ? 2 : 1, OWN_ROWS>(a, p, st, tok);
+  if (p.mode == ALONE) return launch_shape<D, 1, ALONE>(a, p, st, tok);
+  if constexpr (D < 256) {
+    if (p.mode == MERGED8) return launch_shape<D, 1, MERGED8>(a, p, st, tok);
+  }
+  return launch_shape<D, 1, MERGED>(a, p, st, tok);
 }
 
 template <int D>
 static hipError_t launch_dim(const KvAttnArgs& a, const KvPlan& p, hipStream_t st, int tok) {
-  constexpr int WIDE = D < 256 ? 2 : 1;
-  const hipError_t e = p.mode == OWN_ROWS ? launch_shape<D, WIDE, OWN_ROWS>(a, p, st, tok)
-                       : p.rt == 1 ? launch_few<D, 1>(a, p, st, tok) : launch_few<D, WIDE>(a, p, st, tok);
+  const hipError_t e = launch_mode<D>(a, p, st, tok);
   if (e != hipSuccess || p.parts == 0) return e;
   const int groups = (p.tile_rows * D + 511) / 512;
   return launch_k(kv_join_kernel<D>, dim3(static_cast<unsigned>(p.work * groups)), dim3(64 * kWaves), st,

@@ -178,7 +178,7 @@ def test_attention(news, lens, D, heads, group, page, dtype, rotate):
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("seqs,heads,group,new,longest",
                          [(3, 2, 4, 1, 9000), (300, 1, 3, 1, 13000), (40, 2, 4, 5, 6200), (40, 2, 12, 5, 13000),
-                          (2, 2, 8, 5, 2500)])
+                          (2, 2, 8, 5, 2500), (70, 4, 4, 1, 1500)])
 def test_long_lengths_among_short_ones(seqs, heads, group, new, longest, D, dtype):
     """One long sequence, the others short, of length 0 or without new tokens: the pieces of the waves
     begin and end anywhere, and hold many sequences or a part of one."""
