@@ -334,6 +334,26 @@ def test_values_that_are_not_numbers():
         assert out[4, 1].isnan().all() and out.isnan().sum() == 128
 
 
+@pytest.mark.parametrize("n,L", [(30, 50), (1, 200), (1, 6000)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_queries_that_are_not_finite(D, n, L):
+    """An infinity times codes of either sign has no softmax: its row is NaN, the others are as before."""
+    g = gen(15)
+    for rotate in (True, False):
+        cache = R.new_cache(-(-L // 64) + 1, 64, 2, D, rotate)
+        R.fill(cache, g, 2.0)
+        starts, table = R.batch(g, cache, [n], [L])
+        q = heads_of(g, n, 4, D, torch.float32, False)
+        clean, _ = run(cache, q, starts, [L], table)
+        for bad in (math.inf, -math.inf, math.nan):
+            x = q.clone()
+            x[n - 1, 2, 7] = bad
+            out, lse = run(cache, x, starts, [L], table)
+            assert out[n - 1, 2].isnan().all() and lse[n - 1, 2].isnan()
+            out[n - 1, 2] = clean[n - 1, 2]
+            assert torch.equal(out, clean)
+
+
 def test_what_a_compute_unit_held_before_does_not_matter():
     """Parts of a chunk whose page does not exist are not loaded: after a call over codes and scales of
     all ones (NaN) and of the largest numbers, the next one's results are its own."""
