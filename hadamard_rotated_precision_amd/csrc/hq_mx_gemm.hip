@@ -5,7 +5,7 @@
 // lane: row lane % 16, the block of group lane / 16. It scales and adds by itself, so nothing but the
 // loads stands beside it. Products and the sums of a block are exact (multiples of 1/4 below 2^11);
 // its sum of 128 products was within 2^-25 of the sum of their magnitudes on random codes and scales.
-// What bounds it: at 16384^3 the matrix instruction (4.4 PFLOP/s), at 8192^3 (3.75) that and a whole
+// What bounds it: at 16384^3 the matrix instruction (4.5 PFLOP/s), at 8192^3 (3.8) that and a whole
 // number of rounds of tiles. P is the operand along the accumulator's registers (b: output columns, four consecutive ones per
 // lane), Q the one along the lanes (a: output rows).
 #include "hq_device.hpp"
@@ -31,9 +31,11 @@ struct MxGemmArgs {
   float* part;             // several splits: their sums, M x N each, joined by mx_join_kernel
 };
 
-// LDS rows of 128 bytes (256 of K); the 16-byte chunk index is XORed with (row / 2) % 8, so
-// the 128-bit reads of 16 consecutive rows at one chunk meet 16 different bank groups.
-__device__ inline int lds_at(int row, int chunk) { return row * 128 + ((chunk ^ ((row >> 1) & 7)) << 4); }
+// LDS rows of 128 bytes (256 of K); the place of a 16-byte chunk is XORed with (row / 2) % 8, so the
+// 128-bit reads of 16 lanes served at once, of consecutive rows at one place or of some at the next,
+// meet 16 different bank groups (with the chunks in order a sixth of the time went into conflicts:
+// 8192^3 292 us, so 286, 3.84 PFLOP/s).
+__device__ inline int lds_at(int row, int place) { return row * 128 + ((place ^ ((row >> 1) & 7)) << 4); }
 
 // One dword per lane straight into LDS (lane l at lds + 4 l).
 __device__ inline void lds_dma4(__amdgpu_buffer_rsrc_t rs, int8_t* lds, int voffset) {
@@ -101,8 +103,9 @@ __global__ __launch_bounds__(64 * NWP * NWQ * KS, 2) void mx_gemm_kernel(MxGemmA
   const __amdgpu_buffer_rsrc_t ssq = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<uint8_t*>(g.q.scales + q0 * g.q.lds), 0, rows_q * lsq, kBufferFlags);
   // lane's place in a 1 KB load: 8 rows of 128 bytes; it fetches the chunk its swizzled slot holds
-  // (the same for every load: rows advance by multiples of 16)
-  const int dr = 8 * w + (lane >> 3), dc = ((lane & 7) ^ ((dr >> 1) & 7)) << 4;
+  // (the same for every load: rows advance by multiples of 16). Place i of a row holds chunk 2 i, place
+  // 4 + i chunk 2 i + 1.
+  const int dr = 8 * w + (lane >> 3), place = (lane & 7) ^ ((dr >> 1) & 7), dc = ((place << 1 | place >> 2) & 7) << 4;
   const int vp = dr * ldp + dc, vq = dr * ldq + dc;
   const int KB = static_cast<int>((g.K + 31) >> 5);        // blocks: 16 bytes and a scale each
   // this split's steps
@@ -135,8 +138,8 @@ __global__ __launch_bounds__(64 * NWP * NWQ * KS, 2) void mx_gemm_kernel(MxGemmA
   // a lane's blocks are 2 lg and 2 lg + 1 of the step's eight, the same for both operands. The swizzle is
   // that of row lr for every tile of 16 rows, so a lane has two offsets and a tile adds a constant (with
   // an address for each tile the registers ran out and the loop read scratch memory: 8192^3 took 364 us,
-  // now 293, 3.75 PFLOP/s)
-  const int at0 = lds_at(lr, 2 * lg), at1 = lds_at(lr, 2 * lg + 1), at_s = lr * 8 + 2 * lg;
+  // without 293)
+  const int at0 = lds_at(lr, lg), at1 = lds_at(lr, lg + 4), at_s = lr * 8 + 2 * lg;
   auto frag = [&](const int8_t* base, const int8_t* scales, int tile) {
     Fragment f;
     f.x[0] = *reinterpret_cast<const v4i*>(base + at0 + tile * 2048);
