@@ -97,14 +97,13 @@ struct KvTile {
   __device__ int64_t token(const KvAttnArgs& g, int r) const { return s.first + r / g.group; }
   __device__ int q_head(const KvAttnArgs& g, int r) const { return head * g.group + r % g.group; }
   // tokens [from, to) that query row i of the sequence sees, and the chunks that a row of the tile sees
-  __device__ int end_of(int i) const { return static_cast<int>(max<int64_t>(0, min<int64_t>(s.len, s.pos0 + i + 1))); }
-  __device__ int start_of(const KvAttnArgs& g, int i) const {
-    return g.window ? static_cast<int>(max<int64_t>(0, s.pos0 + i + 1 - g.window)) : 0;
-  }
+  __device__ int end_of(int i) const { return kv_end_of(s, i); }
+  __device__ int start_of(const KvAttnArgs& g, int i) const { return kv_start_of(s, i, g.window); }
+  __device__ int last_row(const KvAttnArgs& g) const { return (min(r0 + g.tile_rows, rows) - 1) / g.group; }
   __device__ int first_chunk(const KvAttnArgs& g) const { return start_of(g, r0 / g.group) / kChunk; }
-  __device__ int end_token(const KvAttnArgs& g) const { return end_of((min(r0 + g.tile_rows, rows) - 1) / g.group); }
+  __device__ int end_token(const KvAttnArgs& g) const { return end_of(last_row(g)); }
   __device__ int chunks(const KvAttnArgs& g) const {
-    return r0 < rows ? max(0, (end_token(g) + kChunk - 1) / kChunk - first_chunk(g)) : 0;
+    return r0 < rows ? kv_chunks(s, r0 / g.group, last_row(g), g.window, kChunk).count : 0;
   }
 };
 
@@ -377,21 +376,21 @@ struct KvStage {
 
 // The pages of a sequence, 64 entries of its table at a time in the lanes: an entry is a lane's, read
 // without a wait. (A load for each chunk would be waited for behind the chunk's own loads, or, through the
-// scalar cache, took a third of an iteration.)
+// scalar cache, took a third of an iteration.) Nothing is read before a token is asked for: a wave without
+// a chunk reads no table, and there may be none.
 struct KvPages {
   const int32_t* table;
   int64_t ld, pages;
   int shift, heads, head;
-  int from;          // first entry held
+  int from;          // first entry held; at first far below any
   int32_t held;      // entry from + lane; -1 past the table's end
-  __device__ KvPages(const KvAttnArgs& g, const KvTile& tile, int at)
-      : table(g.table + tile.seq * g.table_ld), ld(g.table_ld), pages(g.pages), shift(g.shift), heads(g.heads), head(tile.head) {
-    fetch(at >> shift);
-  }
+  __device__ KvPages(const KvAttnArgs& g, const KvTile& tile)
+      : table(g.table + tile.seq * g.table_ld), ld(g.table_ld), pages(g.pages), shift(g.shift), heads(g.heads), head(tile.head),
+        from(-(1 << 30)), held(-1) {}
   __device__ void fetch(int entry) {
     from = entry;
     const int64_t mine = static_cast<int64_t>(entry) + (threadIdx.x & 63);
-    held = mine < ld ? table[mine] : -1;
+    held = kv_entry_in_table(mine, ld) ? table[mine] : -1;
   }
   // Row of token `at` >= 0, or -1; `at` is the same in all lanes.
   __device__ int64_t row(int at) {
@@ -464,7 +463,7 @@ __device__ __forceinline__ void attend(const KvAttnArgs& g, const KvTile& tile, 
   const int r0 = tile.r0 + (MODE == OWN_ROWS ? w * ROWS : 0);     // of this wave
   const KvSequence& s = tile.s;
   const int wg_to = tile.end_token(g);
-  KvPages pages(g, tile, (begin + (MERGE ? w : 0)) * kChunk);
+  KvPages pages(g, tile);
 
   // One chunk: its loads have landed (and, where the waves share it, everybody's), those of the next go
   // out into the other stage, whose last reads are done.
@@ -774,7 +773,7 @@ __device__ __forceinline__ void attend(const KvAttnArgs& g, const KvTile& tile, 
 
   if (__any(bad)) {
     for (int at = begin * kChunk; at < min(end * kChunk, any_to); ++at) {
-      const int64_t row = pages.row(at);
+      const int64_t row = kv_row_of_token(at, g.table + tile.seq * g.table_ld, g.table_ld, g.pages, g.shift, g.heads, tile.head);
       if (row < 0) continue;
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt)

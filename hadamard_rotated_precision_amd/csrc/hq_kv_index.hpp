@@ -19,10 +19,12 @@ HQ_BOTH int64_t kv_row_of_slot(int64_t slot, int64_t pages, int shift, int heads
   return ((((slot >> shift) * heads) + head) << shift) + (slot & ((int64_t{1} << shift) - 1));
 }
 
+// Whether a sequence's table has this entry.
+HQ_BOTH bool kv_entry_in_table(int64_t entry, int64_t table_ld) { return entry >= 0 && entry < table_ld; }
 // The entry of a sequence's table that names the page of its token `at`, or -1 where the table ends before.
 HQ_BOTH int64_t kv_entry_of_token(int at, int64_t table_ld, int shift) {
   const int64_t p = at >> shift;
-  return at < 0 || p >= table_ld ? -1 : p;
+  return kv_entry_in_table(p, table_ld) ? p : -1;
 }
 // Row of token `at` in the page that the entry names, or -1 where that is no page of the cache.
 HQ_BOTH int64_t kv_row_in_page(int at, int32_t page, int64_t pages, int shift, int heads, int head) {
@@ -56,6 +58,21 @@ HQ_BOTH KvSequence kv_sequence(int32_t start, int32_t end, int32_t len, int64_t 
   s.pos0 = l - (ok ? all : 0);
   s.len = static_cast<int>(l < max_len ? l : max_len);
   return s;
+}
+
+// Tokens [kv_start_of, kv_end_of) are those that query row i sees; both lie in [0, s.len], whatever the
+// position (a length that the bound cuts may be any).
+HQ_BOTH int kv_cut(const KvSequence& s, int64_t at) { return static_cast<int>(at < 0 ? 0 : at < s.len ? at : s.len); }
+HQ_BOTH int kv_end_of(const KvSequence& s, int i) { return kv_cut(s, s.pos0 + i + 1); }
+HQ_BOTH int kv_start_of(const KvSequence& s, int i, int window) { return window ? kv_cut(s, s.pos0 + i + 1 - window) : 0; }
+
+// The chunks of `size` tokens that one of the query rows first .. last sees.
+struct KvChunks {
+  int first, count;
+};
+HQ_BOTH KvChunks kv_chunks(const KvSequence& s, int first, int last, int window, int size) {
+  const int from = kv_start_of(s, first, window), to = kv_end_of(s, last);
+  return KvChunks{from / size, from < to ? (to + size - 1) / size - from / size : 0};
 }
 
 }  // namespace hq

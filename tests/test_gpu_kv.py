@@ -550,3 +550,38 @@ def test_empty_batches():
     out = torch.full_like(q, 7.0)
     cache.attend(q, out, ints([0, 2]), ints([0]), torch.empty(1, 0, dtype=torch.int32, device=DEV), max_q=2, max_len=0)
     assert not out.any()
+
+
+@pytest.mark.parametrize("rows,longest", [(1, 200), (7, 200), (1, 9000), (40, 200), (40, 9000)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_lengths_far_past_the_bound_with_windows(D, rows, longest):
+    """Positions near 2^31 see nothing of the tokens that the bound leaves, through a window that ends
+    behind them; a window that reaches back to them changes nothing."""
+    g = gen(20)
+    cache = R.new_cache(-(-longest // 64), 64, 2, D)
+    R.fill(cache, g, 2.0)
+    starts, table = R.batch(g, cache, [rows], [longest])
+    table = table.repeat(3, 1)
+    starts = [rows * s for s in range(4)]
+    q = heads_of(g, starts[-1], 4, D, torch.bfloat16, False)
+    far = [2 ** 31 - 1, 2 ** 31 - 64, 2 ** 30]
+    for window in (1, 16, 64, 1000):
+        out, lse = run(cache, q, starts, far, table, max_len=longest, window=window)
+        assert not out.any() and (lse == -math.inf).all()
+    whole = run(cache, q, starts, far, table, max_len=longest)
+    assert all(torch.equal(a, b) for a, b in zip(whole, run(cache, q, starts, far, table, max_len=longest, window=2 ** 31 - 1)))
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_no_table_where_nothing_may_be_seen(D, rows):
+    """With a bound of 0 on the lengths the table may be missing, whatever its pitch."""
+    cache = R.new_cache(4, 16, 2, D)
+    q = heads_of(gen(21), rows, 4, D, torch.bfloat16, False)
+    out, lse = torch.full_like(q, 7.0), torch.full((rows, 4), 7.0, device=DEV)
+    starts, lens = ints([0, rows]), ints([100])
+    b = cache._batch(1, 4, rows, 0)
+    b.q_starts, b.lens, b.table, b.table_ld = starts.data_ptr(), lens.data_ptr(), None, 100
+    B.check(T._launch(B.hq_kv_attention, q, None, q.data_ptr(), T.HQ_DT[q.dtype], rows, *q.stride()[:2], cache.st, b,
+                      out.data_ptr(), T.HQ_DT[out.dtype], lse.data_ptr(), None, 0), "hq_kv_attention")
+    assert not out.any() and (lse == -math.inf).all()

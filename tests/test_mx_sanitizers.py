@@ -91,3 +91,69 @@ def test_wrong_slots_pages_and_lengths_stay_inside(tmp_path):
     r = subprocess.run([exe], capture_output=True, text=True)
     print(r.stdout + r.stderr)
     assert r.returncode == 0 and r.stdout.strip() == "ok"
+
+
+# What a wave of the attention kernel does before its first load: the chunks of a tile of rows, the wave's
+# first one (waves that share rows take every eighth), and the 64 entries of the table around it.
+CHUNKS = r'''
+#include "hq_kv_index.hpp"
+#include <cstdio>
+#include <vector>
+#define CHECK(x) do { if (!(x)) { std::printf("line %d: %s\n", __LINE__, #x); return 1; } } while (0)
+using namespace hq;
+int main() {
+  const int kSize = 64;
+  long waves = 0;
+  for (int32_t len : {INT32_MIN, -1, 0, 1, 63, 64, 65, 1000, 1 << 30, INT32_MAX - 64, INT32_MAX - 1, INT32_MAX})
+    for (int32_t rows : {1, 2, 9, 1000})
+      for (int window : {0, 1, 16, 64, 65, 1000, INT32_MAX - 1, INT32_MAX})
+        for (int max_len : {0, 1, 63, 64, 200, 5000, 1 << 30})
+          for (int max_q : {1, 4, 1000}) {
+            const KvSequence s = kv_sequence(5, 5 + rows, len, 2000, max_q, max_len);
+            CHECK(s.n == (rows < max_q ? rows : max_q));
+            for (int first = 0; first < s.n; first += 1 + s.n / 3) {
+              const int last = first + 15 < s.n ? first + 15 : s.n - 1;
+              for (int i : {first, last, last + 2000000000}) {      // rows behind the last are asked about too
+                const int from = kv_start_of(s, i, window), to = kv_end_of(s, i);
+                CHECK(from >= 0 && from <= s.len && to >= 0 && to <= s.len);
+                const int64_t p = s.pos0 + i;
+                for (int64_t j : {int64_t{0}, int64_t{1}, int64_t{from} - 1, int64_t{from}, int64_t{to} - 1, int64_t{to}})
+                  if (j >= 0 && j < s.len) CHECK((j >= from && j < to) == (j <= p && (!window || j > p - window)));
+              }
+              const KvChunks c = kv_chunks(s, first, last, window, kSize);
+              CHECK(c.first >= 0 && c.count >= 0 && c.first <= (1 << 30) / kSize);
+              if (max_len == 0) CHECK(c.count == 0);
+              for (int w = 0; w < 8; ++w) {
+                if (w >= c.count) continue;
+                const int at = (c.first + w) * kSize;
+                CHECK(at >= 0 && at < s.len);
+                ++waves;
+                for (int shift : {4, 6, 20})
+                  for (int64_t ld : {0, 1, 7}) {
+                    std::vector<int32_t> table(ld, 0);
+                    for (int lane = 0; lane < 64; ++lane) {
+                      const int64_t entry = (at >> shift) + static_cast<int64_t>(lane);
+                      if (kv_entry_in_table(entry, ld)) CHECK(table.at(entry) == 0);
+                    }
+                  }
+              }
+            }
+          }
+  for (int64_t e : {INT64_MIN, -(int64_t{1} << 31), int64_t{-1}, int64_t{7}, int64_t{1} << 31, INT64_MAX}) CHECK(!kv_entry_in_table(e, 7));
+  CHECK(waves > 1000);
+  std::puts("ok");
+  return 0;
+}
+'''
+
+
+def test_no_chunk_of_any_length_and_window_lies_outside(tmp_path):
+    """Lengths up to 2^31 - 1 with windows: positions past the bound on the lengths give no chunk, and no
+    arithmetic on them overflows."""
+    src, exe = tmp_path / "chunks.cpp", str(tmp_path / "chunks")
+    src.write_text(CHUNKS)
+    san = SAN if LIBASAN else []
+    subprocess.run(["g++", "-std=c++17", "-Wall", "-I" + CSRC, str(src), "-o", exe] + san, check=True)
+    r = subprocess.run([exe], capture_output=True, text=True)
+    print(r.stdout + r.stderr)
+    assert r.returncode == 0 and r.stdout.strip() == "ok"
