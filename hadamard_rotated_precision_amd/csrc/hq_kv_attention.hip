@@ -85,24 +85,25 @@ __device__ inline void store8_any(void* p, int dt, int64_t i, const float (&v)[8
 typedef const __attribute__((address_space(4))) int32_t* ConstInts;
 __device__ inline ConstInts constant(const int32_t* p) { return (ConstInts)(reinterpret_cast<uintptr_t>(p)); }
 
-// Rows from row r0 of a sequence's n x group (token by token), and a head of the cache.
+// Rows from row r0 of a sequence's n x group (token by token), and a head of the cache. Inlined by force: a call
+// puts it into scratch memory.
 struct KvTile {
   KvSequence s;
   int seq, head, r0, rows;      // rows: of the sequence
-  __device__ KvTile(const KvAttnArgs& g, int seq_, int tile, int head_) : seq(seq_), head(head_) {
+  __device__ __forceinline__ KvTile(const KvAttnArgs& g, int seq_, int tile, int head_) : seq(seq_), head(head_) {
     s = kv_sequence(constant(g.q_starts)[seq], constant(g.q_starts)[seq + 1], constant(g.lens)[seq], g.tokens, g.max_q, g.max_len);
     r0 = tile * g.tile_rows;
     rows = s.n * g.group;
   }
-  __device__ int64_t token(const KvAttnArgs& g, int r) const { return s.first + r / g.group; }
-  __device__ int q_head(const KvAttnArgs& g, int r) const { return head * g.group + r % g.group; }
+  __device__ __forceinline__ int64_t token(const KvAttnArgs& g, int r) const { return s.first + r / g.group; }
+  __device__ __forceinline__ int q_head(const KvAttnArgs& g, int r) const { return head * g.group + r % g.group; }
   // tokens [from, to) that query row i of the sequence sees, and the chunks that a row of the tile sees
-  __device__ int end_of(int i) const { return kv_end_of(s, i); }
-  __device__ int start_of(const KvAttnArgs& g, int i) const { return kv_start_of(s, i, g.window); }
-  __device__ int last_row(const KvAttnArgs& g) const { return (min(r0 + g.tile_rows, rows) - 1) / g.group; }
-  __device__ int first_chunk(const KvAttnArgs& g) const { return start_of(g, r0 / g.group) / kChunk; }
-  __device__ int end_token(const KvAttnArgs& g) const { return end_of(last_row(g)); }
-  __device__ int chunks(const KvAttnArgs& g) const {
+  __device__ __forceinline__ int end_of(int i) const { return kv_end_of(s, i); }
+  __device__ __forceinline__ int start_of(const KvAttnArgs& g, int i) const { return kv_start_of(s, i, g.window); }
+  __device__ __forceinline__ int last_row(const KvAttnArgs& g) const { return (min(r0 + g.tile_rows, rows) - 1) / g.group; }
+  __device__ __forceinline__ int first_chunk(const KvAttnArgs& g) const { return start_of(g, r0 / g.group) / kChunk; }
+  __device__ __forceinline__ int end_token(const KvAttnArgs& g) const { return end_of(last_row(g)); }
+  __device__ __forceinline__ int chunks(const KvAttnArgs& g) const {
     return r0 < rows ? kv_chunks(s, r0 / g.group, last_row(g), g.window, kChunk).count : 0;
   }
 };
@@ -604,7 +605,7 @@ __device__ __forceinline__ void attend(const KvAttnArgs& g, const KvTile& tile, 
 #pragma unroll
     for (int i = 0; i < DT; ++i) o[rt][i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
   }
-  bool bad = false;      // a token that not every row sees has a scale that is not a number
+  bool bad = false;      // a token that not every row sees has a scale whose values may not be finite
   // masked: not every row of the wave sees every token of the chunk.
   auto compute = [&](bool masked, const int8_t* x, const bool (&ok)[4], int t0) {
     // scores of tokens 16 i + 4 r + lg
@@ -680,8 +681,9 @@ __device__ __forceinline__ void attend(const KvAttnArgs& g, const KvTile& tile, 
 
     // Where not every row sees every token: what lies in LDS for a token that no row sees may be
     // anything (times a large scale infinite, and 0 times that is NaN), so its scale becomes a small one.
-    // A scale that is not a number must not reach the rows that do not see its token: it counts as a
-    // token of zeros (its codes are), and the rows that see it are made NaN by themselves below.
+    // A scale that is not a number, or of 2^126 and more (4 times it is past bf16), must not reach the rows
+    // that do not see its token: its values become nothing here, and the rows that see it get them by themselves
+    // below.
     // O^T += V^T P^T: 32 tokens an instruction, tokens (2 h + j / 4, j % 4) at a lane's element j
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -704,9 +706,9 @@ __device__ __forceinline__ void attend(const KvAttnArgs& g, const KvTile& tile, 
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const int at = 16 * (2 * h + i) + 4 * r;
-            const bool any = ok[2 * h + i] && at < high && at >= low, nan = (sv[i][r] << 1) >= 0xFF000000u;
-            bad |= any && nan;
-            if (nan || !any) sv[i][r] = 0u;
+            const bool any = ok[2 * h + i] && at < high && at >= low, past = (sv[i][r] << 1) >= 0xFD000000u;
+            bad |= any && past;
+            if (past || !any) sv[i][r] = 0u;
           }
       }
       uint32_t y[4][2][Stage::VD];      // of tokens (i, r), (i, r + 1), four such pairs
@@ -747,6 +749,11 @@ __device__ __forceinline__ void attend(const KvAttnArgs& g, const KvTile& tile, 
     }
   };
 
+  // whether not every row of the wave sees every token of a chunk
+  auto cut = [&](const int64_t (&r)[4], int t0) {
+    return !(r[0] >= 0 && r[1] >= 0 && r[2] >= 0 && r[3] >= 0) || t0 + kChunk > all_to || t0 < all_from;
+  };
+  auto seen = [&](int t0) { return MODE != OWN_ROWS || (t0 < any_to && t0 + kChunk > any_from); };
   auto step = [&](int c, int8_t* cur, int8_t* other) {
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     if constexpr (MODE == OWN_ROWS) __builtin_amdgcn_s_barrier();
@@ -757,9 +764,9 @@ __device__ __forceinline__ void attend(const KvAttnArgs& g, const KvTile& tile, 
     }
     __builtin_amdgcn_sched_barrier(0);
     const int t0 = c * kChunk;
-    if (MODE != OWN_ROWS || (t0 < any_to && t0 + kChunk > any_from)) {
+    if (seen(t0)) {
       const bool ok[4] = {row[0] >= 0, row[1] >= 0, row[2] >= 0, row[3] >= 0};
-      compute(!(ok[0] && ok[1] && ok[2] && ok[3]) || t0 + kChunk > all_to || t0 < all_from, cur, ok, t0);
+      compute(cut(row, t0), cur, ok, t0);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) row[i] = next[i];
@@ -771,18 +778,66 @@ __device__ __forceinline__ void attend(const KvAttnArgs& g, const KvTile& tile, 
     if (c + STEP < end) step(c + STEP, s1, s0);
   }
 
+  // The values that were left out, token by token from memory: the scores of its tile of 16 once more (token u
+  // of it in register u % 4 of the lanes u / 4), and what the token adds to the rows that see it. It stands here,
+  // behind the loop, because any more code for such scales in the loop itself spilled registers (prompts of
+  // 128 elements took 5 to 15 % longer with fp32, so 1 %).
   if (__any(bad)) {
-    for (int at = begin * kChunk; at < min(end * kChunk, any_to); ++at) {
-      const int64_t row = kv_row_of_token(at, g.table + tile.seq * g.table_ld, g.table_ld, g.pages, g.shift, g.heads, tile.head);
-      if (row < 0) continue;
+    constexpr int NB = D / 32;
+    for (int c = begin + (MERGE ? w : 0); c < end; c += STEP) {
+      const int t0 = c * kChunk;
+      int64_t rows[4];
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
+      for (int i = 0; i < 4; ++i)
+        rows[i] = t0 + 16 * i < wg_to
+                      ? kv_row_of_token(t0 + 16 * i, g.table + tile.seq * g.table_ld, g.table_ld, g.pages, g.shift, g.heads, tile.head)
+                      : -1;
+      if (!seen(t0) || !cut(rows, t0)) continue;
+      for (int i = 0; i < 4; ++i) {
+        const int64_t tile_row = i < 2 ? (i == 0 ? rows[0] : rows[1]) : (i == 2 ? rows[2] : rows[3]);
+        if (tile_row < 0) continue;
+        v4f a[RT];
 #pragma unroll
-        for (int r = 0; r < 4; ++r)                 // element r of o's tiles lies in block DT (4 lg + r) / 32
-          if (at < to[rt] && at >= from[rt] && g.v_scales[row * (D / 32) + DT * (4 * lg + r) / 32] == 255) {
+        for (int rt = 0; rt < RT; ++rt) a[rt] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int d = 0; d < DT; ++d) o[rt][d][r] = __uint_as_float(0x7FC00000u);
+        for (int u = 0; u < KU; ++u) {
+          const int block = 4 * u + (D == 64 ? lg & 1 : lg);
+          const v4i k = *reinterpret_cast<const v4i*>(g.k_codes + (tile_row + lr) * (D / 2) + 16 * block);
+          const int scale = g.k_scales[(tile_row + lr) * NB + block];
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int e = 0; e < QI; ++e) {
+              const v6u& y = qp[rt][u][e];
+              const v8i qv = {static_cast<int>(y[0]), static_cast<int>(y[1]), static_cast<int>(y[2]), static_cast<int>(y[3]),
+                              static_cast<int>(y[4]), static_cast<int>(y[5]), 0, 0};
+              a[rt] = multiply_part(e, k, scale, qv, qb[rt][u][e / 4], a[rt]);
+            }
+        }
+        for (int u = 0; u < 16; ++u) {
+          const int at = t0 + 16 * i + u, from_lane = 16 * (u >> 2) + lr;
+          const uint8_t* const scales = g.v_scales + (tile_row + u) * NB;
+          const uint8_t* const codes = g.v_codes + (tile_row + u) * (D / 2);
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) {
+            const float s0 = (u & 1) ? a[rt][1] : a[rt][0], s1 = (u & 1) ? a[rt][3] : a[rt][2];
+            const float score = __shfl((u & 2) ? s1 : s0, from_lane, 64);
+            if (at >= to[rt] || at < from[rt]) continue;
+            const float weight = __builtin_amdgcn_exp2f(__builtin_fmaf(score, g.scale2, -base[rt]));
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {                 // element r of o's tiles lies in block DT (4 lg + r) / 32
+              const int first = DT * (4 * lg + r), byte = scales[first / 32];
+              if (byte < 253) continue;
+#pragma unroll
+              for (int d = 0; d < DT; ++d) {
+                const uint32_t code = codes[(first + d) / 2] >> (4 * (d & 1));
+                const float x = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, 1.0f, 0)[0];
+                o[rt][d][r] = byte == 255 ? __uint_as_float(0x7FC00000u) : __builtin_fmaf(weight * x, mx_scale(byte), o[rt][d][r]);
+              }
+            }
           }
+        }
+      }
     }
   }
 

@@ -210,6 +210,11 @@ size_t hq_kv_attention_workspace_bytes(const hq_kv_cache *cache, const hq_kv_bat
  * block's largest magnitude), six (2^-28) where q or out is fp32. Probabilities enter it as two bf16
  * numbers (their sum is within 2^-17 of the value) or three (2^-25) beside the values, which are exact
  * in bf16.
+ * A token changes no row that does not see it, whatever its codes and scales hold; one whose scale is
+ * NaN makes the rows that see it NaN (of values: in that block, or all of it if rotated). Accumulators are
+ * sums of exp(s - m) v with m the largest score so far: where such a sum of magnitudes reaches 2^128, and in
+ * elements where a token that a row sees has a value of 2^128 or more (scale bytes 253 and 254 allow
+ * them), the result may be infinite or NaN.
  * Sequences' query rows must not overlap (their results would). */
 hq_status hq_kv_attention(const void *q, int32_t q_dtype, int64_t tokens, int64_t q_token,
                           int64_t q_head, const hq_kv_cache *cache, const hq_kv_batch *batch,

@@ -585,3 +585,32 @@ def test_no_table_where_nothing_may_be_seen(D, rows):
     B.check(T._launch(B.hq_kv_attention, q, None, q.data_ptr(), T.HQ_DT[q.dtype], rows, *q.stride()[:2], cache.st, b,
                       out.data_ptr(), T.HQ_DT[out.dtype], lse.data_ptr(), None, 0), "hq_kv_attention")
     assert not out.any() and (lse == -math.inf).all()
+
+
+@pytest.mark.parametrize("byte,codes", [(253, 0x76), (254, 0x76), (253, 0x55)])
+@pytest.mark.parametrize("n,before", [(12, 0), (80, 0), (12, 9000)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_values_near_and_past_2_to_the_128(D, n, before, byte, codes):
+    """A token whose values lie past fp32 (4 and 6 times its scale) leaves the rows that do not see it as
+    they are, and for those that do may make the elements with such values infinite or NaN, but no others.
+    Below (3 times 2^126) everything counts in full."""
+    g = gen(22)
+    first = before + 20
+    L, at = first + n, first + 5
+    cache = R.new_cache(-(-L // 16), 16, 2, D, False)
+    R.fill(cache, g, 2.0)
+    starts, table = R.batch(g, cache, [n], [L])
+    q = heads_of(g, n, 4, D, torch.float32, False) * 0.3
+    clean, _ = run(cache, q, starts, [L], table)
+    page, row = table[0, at // 16], at % 16
+    cache.v_scales[page, :, row, 1] = byte
+    cache.v_codes[page, :, row, 16:32] = codes
+    out, lse = run(cache, q, starts, [L], table)
+    assert torch.equal(out[:at - first], clean[:at - first])
+    want, want_l, err, err_l = R.attention(cache, q, starts, [L], table, D ** -0.5, 0, out.dtype)
+    free = torch.zeros_like(out, dtype=torch.bool)
+    if codes == 0x76:
+        free[at - first:, :, 32:64] = ~out[at - first:, :, 32:64].isfinite()
+    R.assert_within(out[~free], want[~free], err[~free], "attention")
+    R.assert_within(lse, want_l, err_l, "lse")
+    assert (out[at - first:, :, 32:64] != clean[at - first:, :, 32:64]).all()
