@@ -1081,7 +1081,7 @@ static KvPlan kv_plan(const hq_kv_cache& c, const hq_kv_batch& b) {
   const int64_t rows = static_cast<int64_t>(b.max_q) * (b.q_heads / c.heads);
   const bool few = rows <= (c.head_dim == 256 ? 32 : 64);
   const int64_t seen = b.window ? std::min<int64_t>(b.max_len, static_cast<int64_t>(b.window) + b.max_q) : b.max_len;
-  const int64_t chunks = (seen + kChunk - 1) / kChunk + 1;
+  const int64_t chunks = (seen + kChunk - 1) / kChunk + 1, unwindowed = (static_cast<int64_t>(b.max_len) + kChunk - 1) / kChunk + 1;
   const int64_t fit = 256 * (c.head_dim == 64 ? 3 : c.head_dim == 128 ? 2 : 1);   // workgroups on the chip
   auto shape = [&](int mode) {
     p.mode = mode;
@@ -1093,9 +1093,10 @@ static KvPlan kv_plan(const hq_kv_cache& c, const hq_kv_batch& b) {
   };
   shape(few ? MERGED : OWN_ROWS);
   if (few && c.head_dim < 256 && p.work <= 256 && chunks > kWaves) shape(MERGED8);
-  // (a wave counts its chunks in 32 bits)
+  // (a wave counts its chunks in 32 bits; asked without the window, so that one never brings the line, and a
+  // workspace, where none has neither)
   if (few && chunks > (p.mode == MERGED8 ? 52 + 7 * p.work / 10 : 48 + p.work / 4) &&
-      p.work * chunks < int64_t{1} << 40)
+      p.work * unwindowed < int64_t{1} << 40)
     shape(ALONE);
   if (p.mode == ALONE) {
     p.least = 4;

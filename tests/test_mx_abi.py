@@ -301,3 +301,19 @@ def test_a_window_needs_no_more_workspace_than_none():
         without = B.hq_kv_attention_workspace_bytes(c, batch(**b))
         window = int(2 ** rng.uniform(0, 18))
         assert B.hq_kv_attention_workspace_bytes(c, batch(window=window, **b)) <= without, (b, window)
+
+
+@pytest.mark.skipif("HQ_MX_LIB_PATH" in os.environ, reason="the sanitizer build has no launchers of its own")
+def test_a_window_needs_no_more_workspace_than_none_up_to_every_limit():
+    """The same over all that the checks admit: lengths up to 2^30 and thousands of sequences of many heads."""
+    c = cache(head_dim=64, heads=256, rot=1)
+    far = dict(seqs=1645, q_heads=256, max_q=2, max_len=219732955)
+    assert B.hq_kv_attention_workspace_bytes(c, batch(**far)) == B.hq_kv_attention_workspace_bytes(c, batch(window=10938102, **far))
+    rng = random.Random(2)
+    for _ in range(6000):
+        c = cache(head_dim=rng.choice([64, 128, 256]), heads=int(2 ** rng.uniform(0, 10)), rot=1)
+        b = dict(seqs=int(2 ** rng.uniform(0, 14)), q_heads=c.heads * rng.choice([1, 2, 8]), max_q=int(2 ** rng.uniform(0, 7)),
+                 max_len=int(2 ** rng.uniform(0, 30)))
+        without = B.hq_kv_attention_workspace_bytes(c, batch(**b))
+        for window in (1, int(2 ** rng.uniform(0, 30)), b["max_len"], 2 ** 31 - 1):
+            assert B.hq_kv_attention_workspace_bytes(c, batch(window=window, **b)) <= without, (b, window)
