@@ -137,9 +137,10 @@ bool shapes_ok(int64_t N, int64_t C, int64_t D) { return mx_dims_ok(N, C) && mx_
 // ---------------------------------------------------------------- the cache
 constexpr int64_t kMaxSlots = int64_t{1} << 31;
 
-// Tokens of a call: two vectors of head_dim / 8 threads for each head stay countable in 32 bits.
+// Tokens of a call: two vectors of head_dim / 8 threads for each head, in whole workgroups of 256, are fewer
+// than 2^32 threads, the most that a launch takes.
 bool tokens_ok(int64_t n, const hq_kv_cache& c) {
-  return n >= 0 && n <= kMaxSlots / (static_cast<int64_t>(c.heads) * (c.head_dim / 8));
+  return n >= 0 && n <= ((int64_t{1} << 31) - 128) / (static_cast<int64_t>(c.heads) * (c.head_dim / 8));
 }
 
 hq_status check_cache(const hq_kv_cache* c) {

@@ -317,3 +317,18 @@ def test_a_window_needs_no_more_workspace_than_none_up_to_every_limit():
         without = B.hq_kv_attention_workspace_bytes(c, batch(**b))
         for window in (1, int(2 ** rng.uniform(0, 30)), b["max_len"], 2 ** 31 - 1):
             assert B.hq_kv_attention_workspace_bytes(c, batch(window=window, **b)) <= without, (b, window)
+
+
+@pytest.mark.parametrize("heads,D", [(1, 64), (3, 128), (1024, 256)])
+def test_a_call_of_the_cache_fits_one_launch(heads, D):
+    """A thread takes eight elements of a key or value, 256 of them a workgroup, and a launch has fewer
+    than 2^32 threads: the largest number of tokens that fits passes the checks, the next does not."""
+    most = 0
+    for bit in range(31, -1, -1):
+        n = most + (1 << bit)
+        if -(-2 * n * heads * (D // 8) // 256) * 256 < 1 << 32:
+            most = n
+    c = cache(heads=heads, head_dim=D, rot=1)
+    for n, want in ((most, "HQ_ERR_DEVICE"), (most + 1, "HQ_ERR_SHAPE")):
+        assert name(B.hq_kv_append(FAKE, FAKE, 2, n, 0, 0, 0, 0, FAKE, c, None)) == want
+        assert name(B.hq_kv_read(c, FAKE, n, FAKE, None, 2, None)) == want
