@@ -76,14 +76,11 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvArgs g) {
   }
   float v[8];
   mx_values8(w, v);
+  // divided by D first (exact: codes times at least 2^-135), so that the sums stay below the largest value
   const float s = byte == 255 ? __uint_as_float(0x7FC00000u) : byte ? mx_scale(byte) : 5.87747175e-39f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] *= s;
-  if constexpr (ROT) {
-    rotate_lanes<D>(v, t & 63);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] *= 1.0f / D;
-  }
+  for (int j = 0; j < 8; ++j) v[j] *= ROT ? s * (1.0f / D) : s;
+  if constexpr (ROT) rotate_lanes<D>(v, t & 63);
   if (wanted) store8<T>(out, (at.token * g.heads + at.head) * D + 8 * l, 8, v);
 }
 

@@ -257,14 +257,11 @@ __device__ inline float shfl_fmax(float x, int m) { return fmaxf(x, __shfl_xor(x
 template <int D>
 __device__ inline void finish_row(const KvAttnArgs& g, const KvTile& tile, int row, int l, float total, float m, bool in,
                                   float (&v)[8]) {
-  const float inv = total == 0.0f ? 0.0f : 1.0f / total;     // a row that sees nothing: zeros
+  // a row that sees nothing: zeros. The rotation's 1 / D comes before its sums, which then stay in range
+  const float inv = total == 0.0f ? 0.0f : 1.0f / total * (g.rot > 1 ? 1.0f / D : 1.0f);
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] *= inv;
-  if (g.rot > 1) {
-    rotate_lanes<D>(v, threadIdx.x & 63);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] *= 1.0f / D;
-  }
+  if (g.rot > 1) rotate_lanes<D>(v, threadIdx.x & 63);
   if (!in) return;
   const int64_t at = tile.token(g, row) * (g.heads * g.group) + tile.q_head(g, row);
   store8_any(g.out, g.out_dt, at * D + 8 * l, v);
@@ -855,7 +852,7 @@ __device__ __forceinline__ void attend(const KvAttnArgs& g, const KvTile& tile, 
       const bool in = row < tile.rows;
       if (r0 >= tile.rows) return;                // the whole wave
       float v[D / 4];
-      const float inv = part_at >= 0 ? 1.0f : l[rt] == 0.0f ? 0.0f : 1.0f / l[rt];
+      const float inv = part_at >= 0 ? 1.0f : l[rt] == 0.0f ? 0.0f : 1.0f / l[rt] * (g.rot > 1 ? 1.0f / D : 1.0f);
 #pragma unroll
       for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -868,11 +865,7 @@ __device__ __forceinline__ void attend(const KvAttnArgs& g, const KvTile& tile, 
         if (lg == 0) g.stats[2 * at] = m[rt] == -__builtin_inff() ? m[rt] : base[rt], g.stats[2 * at + 1] = l[rt];
         continue;
       }
-      if (g.rot > 1) {
-        rotate_row<D / 4, 4>(v, lane);
-#pragma unroll
-        for (int j = 0; j < D / 4; ++j) v[j] *= 1.0f / D;
-      }
+      if (g.rot > 1) rotate_row<D / 4, 4>(v, lane);
       if (!in) continue;
       const int64_t at = tile.token(g, row) * (g.heads * g.group) + tile.q_head(g, row);
 #pragma unroll

@@ -614,3 +614,36 @@ def test_values_near_and_past_2_to_the_128(D, n, before, byte, codes):
     R.assert_within(out[~free], want[~free], err[~free], "attention")
     R.assert_within(lse, want_l, err_l, "lse")
     assert (out[at - first:, :, 32:64] != clean[at - first:, :, 32:64]).all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_large_values_come_back_from_the_rotation(D):
+    """One element of 1e38 in a vector: its rotated codes stay below 2^128, and so do the sums that rotate them
+    back, reading or behind the attention."""
+    g = gen(23)
+    cache, n = R.new_cache(2, 16, 1, D), 20
+    x = heads_of(g, n, 1, D, torch.float32)
+    x[3, 0, 7], x[11, 0, D - 1] = 1e38, -1e38
+    slots = torch.randperm(32, generator=g, device=DEV)[:n].contiguous()
+    cache.append(x, x, slots)
+    k, v = torch.empty_like(x), torch.empty_like(x)
+    cache.read(slots, k, v)
+    held = R.values(*R.quantize(x, D))
+    want = R.hadamard(held, D) / D
+    slack = (math.log2(D) + 1) * 2.0 ** -24 * held.abs().sum(-1, keepdim=True) / D
+    for got in (k, v):
+        R.assert_within(got, want, slack + 2.0 ** -24 * (want.abs() + slack) + 2.0 ** -126, "read back")
+    # rows that see one token each, in the form where waves share the rows and in the one where each has its own
+    for rows in (1, 70):
+        at = torch.tensor([3, 11], device=DEV)
+        one = R.new_cache(2, 16, 1, D)
+        one.append(heads_of(g, 2, 1, D, torch.float32, False), x[at].contiguous(), torch.tensor([0, 16], device=DEV))
+        lens, starts = [rows, rows], [0, rows, 2 * rows]
+        table = ints([[0] * 5, [1] * 5])
+        q = heads_of(g, 2 * rows, 4, D, torch.bfloat16, False)
+        out, _ = run(one, q, starts, lens, table, max_len=1, window=rows, dtype=torch.float32)
+        # beside the rotation's steps: a weight split into three parts (2^-25), their products added (three steps that
+        # may cut: 2^-23 each), two steps of the division: below 2^-20 of every element before the rotation
+        for s in (0, 1):
+            err = slack[at[s], 0] + 2.0 ** -20 * (want[at[s], 0].abs() + held[at[s], 0].abs().sum() / D)
+            R.assert_within(out[s * rows:(s + 1) * rows], want[at[s], 0].expand(rows, 4, D), err.expand(rows, 4, D), "attention")
