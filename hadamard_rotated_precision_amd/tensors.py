@@ -844,7 +844,11 @@ class KVCache:
     @staticmethod
     def _batch(seqs, q_heads, max_q, max_len, window=0, scale=1.0):
         b = B.hq_kv_batch()
-        b.seqs, b.q_heads, b.max_q, b.max_len, b.window, b.scale = seqs, q_heads, max_q, max_len, window, scale
+        b.scale = scale
+        for name, x in (("seqs", seqs), ("q_heads", q_heads), ("max_q", max_q), ("max_len", max_len), ("window", window)):
+            if not -1 << 31 <= x < 1 << 31:       # ctypes would cut it
+                raise ValueError("%s is %d, past 32 bits" % (name, x))
+            setattr(b, name, x)
         return b
 
     def attention_workspace(self, seqs, q_heads, max_q, max_len):

@@ -49,3 +49,20 @@ def test_layouts():
     cache = T.KVCache(3, 32, 2, 256, rotate=False, device="cpu")
     assert cache.k_codes.shape == (3, 2, 32, 128) and cache.v_scales.shape == (3, 2, 32, 8)
     assert cache.st.rot == 1 and T.KVCache(3, 32, 2, 256, device="cpu").st.rot == 256
+
+
+def test_bounds_past_32_bits_are_refused():
+    """The library's struct holds 32-bit bounds, and ctypes would cut longer ones: 2^32 + 5 to 5."""
+    cache = T.KVCache(4, 16, 2, 64, device="cpu")
+    q, i = torch.zeros(3, 2, 64), torch.zeros(2, dtype=torch.int32)
+    ws = torch.zeros(1 << 20, dtype=torch.uint8)
+    for name in ("max_q", "max_len", "window"):
+        for value in (1 << 31, (1 << 32) + 5, 1 << 63):
+            kw = dict(dict(max_q=3, max_len=5, window=0), **{name: value})
+            with pytest.raises(ValueError, match=name):
+                cache.attend(q, q.clone(), i, i[:1], i[:1].view(1, 1), ws=ws, **kw)
+    for kw in (dict(max_q=(1 << 32) + 1, max_len=5), dict(max_q=1, max_len=(1 << 32) + 5)):
+        with pytest.raises(ValueError, match="32 bits"):
+            cache.attention_workspace(1, 2, **kw)
+    with pytest.raises(ValueError, match="seqs"):
+        cache.attention_workspace((1 << 32) + 1, 2, max_q=1, max_len=5)
