@@ -645,7 +645,7 @@ class MxTensor:
         are: codes at least rows x 16 ceil(cols / 32) bytes, scales at least rows x the multiple of 16
         from ceil(cols / 32) on. Checks their shapes and, once, on the host, that scale bytes past the
         last block (and, without rotation, codes past the last column) are zero."""
-        if codes is None or (codes_t is None) != (scales_t is None):
+        if codes is None or scales is None or (codes_t is None) != (scales_t is None):
             raise ValueError("codes are needed, and scales with them")
         for name, c, s, n, length in (("", codes, scales, rows, cols), ("_t", codes_t, scales_t, cols, rows)):
             if c is None:

@@ -66,3 +66,15 @@ def test_bounds_past_32_bits_are_refused():
             cache.attention_workspace(1, 2, **kw)
     with pytest.raises(ValueError, match="seqs"):
         cache.attention_workspace((1 << 32) + 1, 2, max_q=1, max_len=5)
+
+
+def test_wrapped_codes_need_their_scales():
+    q = T.MxTensor(8, 64, device="cpu")
+    for t in (q.codes, q.scales, q.codes_t, q.scales_t):
+        t.zero_()
+    assert T.MxTensor.wrap(q.codes, q.scales, 8, 64).scales is q.scales
+    for args, kw in (((q.codes, None, 8, 64), {}), ((None, q.scales, 8, 64), {}),
+                     ((q.codes, q.scales, 8, 64), dict(codes_t=q.codes_t)),
+                     ((q.codes, q.scales, 8, 64), dict(scales_t=q.scales_t))):
+        with pytest.raises(ValueError, match="needed"):
+            T.MxTensor.wrap(*args, **kw)
