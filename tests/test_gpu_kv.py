@@ -647,3 +647,35 @@ def test_large_values_come_back_from_the_rotation(D):
         for s in (0, 1):
             err = slack[at[s], 0] + 2.0 ** -20 * (want[at[s], 0].abs() + held[at[s], 0].abs().sum() / D)
             R.assert_within(out[s * rows:(s + 1) * rows], want[at[s], 0].expand(rows, 4, D), err.expand(rows, 4, D), "attention")
+
+
+@pytest.mark.parametrize("scale", [-0.5, 0.0, 2.0])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_scales_of_either_sign_where_waves_have_rows_of_their_own(D, dtype, scale):
+    g = gen(24)
+    for rotate in (True, False):
+        cache = R.new_cache(30, 16, 2, D, rotate)
+        R.fill(cache, g, 2.0)
+        starts, table = R.batch(g, cache, [90, 3], [150, 200])
+        check(cache, heads_of(g, 93, 4, D, dtype, False) * 0.2, starts, [150, 200], table, scale=scale)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("news,lens", [([1, 3], [300, 77]), ([1], [6000]), ([90], [200])])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_queries_with_outlier_channels(D, news, lens, dtype):
+    """Channels of the queries 20 and 1000 times the others, where the cache holds outlier channels too and
+    where it holds none: what a query's part of 6 bits leaves is counted by its block's largest element."""
+    g = gen(25)
+    for rotate in (True, False):
+        page = 64
+        cache = R.new_cache(sum(-(-n // page) for n in lens) + 1, page, 2, D, rotate)
+        starts, table = R.batch(g, cache, news, lens)
+        for s, n in enumerate(lens):
+            at = torch.arange(n, device=DEV)
+            k = heads_of(g, n, 2, D, torch.bfloat16, rotate)
+            cache.append(k, heads_of(g, n, 2, D, torch.bfloat16), table[s].long()[at // page] * page + at % page)
+        q = heads_of(g, starts[-1], 8, D, torch.float32) * 0.02
+        q[..., 40] *= 1000
+        check(cache, q.to(dtype), starts, lens, table)
