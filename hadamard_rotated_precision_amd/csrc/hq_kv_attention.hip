@@ -602,7 +602,7 @@ __device__ __forceinline__ void attend(const KvAttnArgs& g, const KvTile& tile, 
 #pragma unroll
     for (int i = 0; i < DT; ++i) o[rt][i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
   }
-  bool bad = false;      // a token that not every row sees has a scale whose values may not be finite
+  uint32_t bad = 0;      // largest scale byte (bits 24 to 31) of V's tokens that not every row sees
   // masked: not every row of the wave sees every token of the chunk.
   auto compute = [&](bool masked, const int8_t* x, const bool (&ok)[4], int t0) {
     // scores of tokens 16 i + 4 r + lg
@@ -704,7 +704,7 @@ __device__ __forceinline__ void attend(const KvAttnArgs& g, const KvTile& tile, 
           for (int r = 0; r < 4; ++r) {
             const int at = 16 * (2 * h + i) + 4 * r;
             const bool any = ok[2 * h + i] && at < high && at >= low, past = (sv[i][r] << 1) >= 0xFD000000u;
-            bad |= any && past;
+            bad = max(bad, any ? sv[i][r] << 1 : 0u);
             if (past || !any) sv[i][r] = 0u;
           }
       }
@@ -778,16 +778,20 @@ __device__ __forceinline__ void attend(const KvAttnArgs& g, const KvTile& tile, 
   // The values that were left out, token by token from memory: the scores of its tile of 16 once more (token u
   // of it in register u % 4 of the lanes u / 4), and what the token adds to the rows that see it. It stands here,
   // behind the loop, because any more code for such scales in the loop itself spilled registers (prompts of
-  // 128 elements took 5 to 15 % longer with fp32, so 1 %).
-  if (__any(bad)) {
+  // 128 elements took 11 % longer with fp32, so none; with bf16 1 to 3 either way).
+  if (__any(bad >= 0xFD000000u)) {
     constexpr int NB = D / 32;
+    // copies that the compiler takes for other values: what it would keep for this over the loop is formed here
+    const uint8_t *kc = g.k_codes, *vc = g.v_codes, *ks = g.k_scales, *vs = g.v_scales;
+    const int32_t* tb = g.table + tile.seq * g.table_ld;
+    asm volatile("" : "+s"(kc), "+s"(vc), "+s"(ks), "+s"(vs), "+s"(tb));
     for (int c = begin + (MERGE ? w : 0); c < end; c += STEP) {
       const int t0 = c * kChunk;
       int64_t rows[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         rows[i] = t0 + 16 * i < wg_to
-                      ? kv_row_of_token(t0 + 16 * i, g.table + tile.seq * g.table_ld, g.table_ld, g.pages, g.shift, g.heads, tile.head)
+                      ? kv_row_of_token(t0 + 16 * i, tb, g.table_ld, g.pages, g.shift, g.heads, tile.head)
                       : -1;
       if (!seen(t0) || !cut(rows, t0)) continue;
       for (int i = 0; i < 4; ++i) {
@@ -799,8 +803,8 @@ __device__ __forceinline__ void attend(const KvAttnArgs& g, const KvTile& tile, 
 #pragma unroll
         for (int u = 0; u < KU; ++u) {
           const int block = 4 * u + (D == 64 ? lg & 1 : lg);
-          const v4i k = *reinterpret_cast<const v4i*>(g.k_codes + (tile_row + lr) * (D / 2) + 16 * block);
-          const int scale = g.k_scales[(tile_row + lr) * NB + block];
+          const v4i k = *reinterpret_cast<const v4i*>(kc + (tile_row + lr) * (D / 2) + 16 * block);
+          const int scale = ks[(tile_row + lr) * NB + block];
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
@@ -813,8 +817,8 @@ __device__ __forceinline__ void attend(const KvAttnArgs& g, const KvTile& tile, 
         }
         for (int u = 0; u < 16; ++u) {
           const int at = t0 + 16 * i + u, from_lane = 16 * (u >> 2) + lr;
-          const uint8_t* const scales = g.v_scales + (tile_row + u) * NB;
-          const uint8_t* const codes = g.v_codes + (tile_row + u) * (D / 2);
+          const uint8_t* const scales = vs + (tile_row + u) * NB;
+          const uint8_t* const codes = vc + (tile_row + u) * (D / 2);
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) {
             const float s0 = (u & 1) ? a[rt][1] : a[rt][0], s1 = (u & 1) ? a[rt][3] : a[rt][2];
