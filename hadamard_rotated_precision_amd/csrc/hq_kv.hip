@@ -4,8 +4,9 @@
 // each block quantized as hq_mx.hip does: D / 8 lanes hold eight elements each, so strides 1, 2, 4
 // are in registers, the others across lanes, and a block's largest magnitude is that of a quad.
 //
-// What bounds it: bytes (16384 tokens of 8 heads of 128, bf16: 85 MB in 25 us each way, 3.4 TB/s); for
-// a decode batch, the launch (48 tokens: 3 us).
+// What bounds it: the vector pipe, busy for 80 to 90 % of the time (16384 tokens of 8 heads of 128, bf16: 85 MB
+// in 25.7 us to the cache and 23.7 back, where a copy of as many bytes takes 18): the index of a vector and its
+// addresses, 64-bit numbers, serve eight elements only. For a decode batch, the launch (48 tokens: 3 us).
 #include "hq_device.hpp"
 #include "hq_kv_index.hpp"
 #include "hq_launch.hpp"

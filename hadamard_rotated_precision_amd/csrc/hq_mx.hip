@@ -6,10 +6,12 @@
 // bit patterns so that an infinity or a NaN comes out on top); v / s is exact, so a code is the value
 // nearest to v / s without an intermediate rounding.
 //
-// What bounds it: bytes. R x C elements of e bytes are read once, 17/32 R C bytes are written for
-// each layout: both from 8192 x 13824 bf16, rotated, take 100 us to nearest (347 MB, 3.5 TB/s) and 186
-// rounded at random, where the vector pipe is the bound (the two hashes' multiplications at a quarter
-// of its rate, for each pair and layout); the way back 45 us (286 MB, 6.4 TB/s, in part out of caches).
+// What bounds it: R x C elements of e bytes are read once, 17/32 R C bytes are written for each layout.
+// One layout goes at the rate of its bytes (1000 x 5120: 5.8 us, launch included), the way back too (from
+// 8192 x 13824 45 us: 286 MB, 6.4 TB/s, in part out of caches). Both layouts from 8192 x 13824 bf16, rotated,
+// take 100 us to nearest (347 MB, 3.5 TB/s; a copy 72), the vector pipe busy for 78 % of the time and LDS
+// conflicts for 17 % of the cycles, and 180 to 192 rounded at random, where the vector pipe is the bound (95 %: the
+// two hashes' multiplications at a quarter of its rate, for each pair and layout).
 #include "hq_device.hpp"
 #include "hq_launch.hpp"
 #include "hq_mx_device.hpp"
@@ -68,8 +70,8 @@ __global__ __launch_bounds__(256) void mx_quant_rows_kernel(MxQuantArgs g) {
 // either direction, 8 and 16 across lanes.
 template <class T, int ROT, bool RANDOM>
 __global__ __launch_bounds__(256) void mx_quant_kernel(MxQuantArgs g) {
-  // 64 code bytes of a row and of a column: a wave's dwords of the eight columns (rows) of a lane spread over
-  // the banks at a pitch of 80
+  // 64 code bytes of a row and of a column, at a pitch of 80 (16-byte pieces): a wave's dwords of its rows
+  // spread over the banks, those of its columns (neighbouring lanes 8 x 80 bytes apart) meet eight of them
   __shared__ __attribute__((aligned(16))) uint8_t straight[128 * 80], turned[128 * 80];
   __shared__ __attribute__((aligned(4))) uint8_t rs[128][4], cs[128][4];
   const int t = threadIdx.x, cg = t & 15, rg = t >> 4, wave = t >> 6;

@@ -62,7 +62,8 @@ int32_t hq_mx_abi_version(void);
  * v / s, ties to the even code. A block that holds a NaN or an infinity (or a rotated sum past fp32)
  * gets b = 255 and zero codes, so every product that reads it is NaN.
  *
- * Rounding at random (for gradients: the mean of a code is v / s itself): with x = |v| / s and 16
+ * Rounding at random (for gradients: the mean of a code is v / s, less at most 2^-16 of the step between
+ * its neighbours, toward zero, since u has 16 bits; below 2^-17 s it is 0): with x = |v| / s and 16
  * random bits u, x >= 1: the bit pattern of fp32 x plus 64 u, cut to one bit of fraction; x < 1:
  * floor(fp32(2 x + u / 65536)) halves. The bits of row r and column c come from a seed alone:
  *   mix(h): h ^= h >> 16; h *= 2654435761; h ^= h >> 15; h *= 2891336453; h ^= h >> 16
@@ -207,7 +208,9 @@ size_t hq_kv_attention_workspace_bytes(const hq_kv_cache *cache, const hq_kv_bat
  * logarithms of the sums of exp(scale q k).
  * Sums, maxima and accumulators are fp32. Queries enter the matrix instruction beside the keys' codes,
  * in parts of 6 bits with a scale for each block of 32: four parts (their sum is within 2^-18 of the
- * block's largest magnitude), six (2^-28) where q or out is fp32. Probabilities enter it as two bf16
+ * block's largest magnitude, or 2^-125 where that is more), six (2^-28) where q or out is fp32. lse has
+ * the scores' precision: an fp32 lse of 16-bit q and out is no more precise for being fp32. An infinity
+ * or a NaN in a query, or a rotated sum of it past fp32, makes its row NaN. Probabilities enter it as two bf16
  * numbers (their sum is within 2^-17 of the value) or three (2^-25) beside the values, which are exact
  * in bf16.
  * A token changes no row that does not see it, whatever its codes and scales hold; one whose scale is
